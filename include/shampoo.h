@@ -462,6 +462,147 @@ shampoo_status shampoo_selftest_stall_next_stats(shampoo_ctx* ctx);
  */
 shampoo_status shampoo_selftest_stall_next_apply(shampoo_ctx* ctx);
 
+/*
+ * Many-tensor operators beside the Shampoo step: the clipping of a gradient
+ * list to a global norm, and the AdamW step for the parameters that Shampoo is
+ * not used on (embeddings, biases, norms; or all of them).  (The paper has no
+ * counterpart; "Decoupled Weight Decay Regularization", Loshchilov and Hutter, is
+ * AdamW's.)
+ *
+ * Both work on a fixed list of tensors, given by their element counts at create
+ * time.  A call takes the tensors' device pointers, each to contiguous elements
+ * and aligned to its element (16-byte alignment is faster), in any order of
+ * addresses.  Two tensors that a call writes must not overlap, nor one that it
+ * writes and one that it reads (SHAMPOO_EINVAL).  A tensor whose gradient holds
+ * a NaN or Inf is skipped, as in shampoo_update_stats: nothing of it is written, it
+ * does not count in the norm, and the others go on.
+ *
+ * A call checks its arguments and launches its kernels, on the context's stream and
+ * the device that was current at create time; it copies, allocates and waits
+ * for nothing, and can be captured into a CUDA graph (the learning rate and
+ * the pointers are then the captured ones; step counts advance with every replay).
+ * The same inputs give the same bits.  A context holds one pass's work space: calls
+ * and replays of graphs that use the same context must not overlap on the GPU.
+ */
+typedef struct shampoo_clip shampoo_clip;     /* opaque, library-owned */
+typedef struct shampoo_adamw shampoo_adamw;   /* opaque, library-owned */
+
+/*
+ * shampoo_clip_create -- a context for gradient lists of `nparams` tensors.
+ *  numel       host array [nparams] of element counts, each >= 1.
+ *  grad_dtype  element type of every gradient.
+ *  cuda_stream caller-owned cudaStream_t (NULL = legacy default stream).
+ * Synchronises the stream once.
+ */
+shampoo_status shampoo_clip_create(shampoo_clip** out, int nparams, const int64_t* numel,
+                                   shampoo_dtype grad_dtype, void* cuda_stream);
+
+/*
+ * shampoo_clip_norm -- norm = sqrt(sum g^2) over all tensors of the list whose
+ * gradient is finite, left on the device (shampoo_clip_result).  Gradients are
+ * not changed.  Sums are kept in 64 bits (sixteen squares at a time in 32): gradients
+ * whose squares pass the range of a float have a norm too.
+ */
+shampoo_status shampoo_clip_norm(shampoo_clip* clip, const void* const* grads);
+
+/*
+ * shampoo_clip_apply -- the same norm, then g <- g * (max_norm / norm) in place
+ * where norm > max_norm; a bfloat16 product is rounded to nearest.  Gradients
+ * of a norm within max_norm are not written.  max_norm > 0.
+ */
+shampoo_status shampoo_clip_apply(shampoo_clip* clip, void* const* grads, double max_norm);
+
+/*
+ * shampoo_clip_result -- *norm receives the device address of the last call's
+ * norm: one float, library-owned, valid until shampoo_clip_destroy and
+ * overwritten by the next call (in stream order).
+ */
+shampoo_status shampoo_clip_result(shampoo_clip* clip, void** norm);
+
+/*
+ * shampoo_clip_set_stream -- queue later calls on another stream of the
+ * same device (a capturing one too).  The caller orders it behind the one
+ * that holds the context's earlier calls.
+ */
+shampoo_status shampoo_clip_set_stream(shampoo_clip* clip, void* cuda_stream);
+
+/* Tensors skipped by the last call because their gradient was not finite.  Synchronises. */
+shampoo_status shampoo_clip_nonfinite_status(shampoo_clip* clip, int* n_params_skipped);
+const char* shampoo_clip_last_error(const shampoo_clip* clip);
+void shampoo_clip_destroy(shampoo_clip* clip);   /* NULL is a no-op */
+
+/*
+ * shampoo_adamw_create -- AdamW over `nparams` float32 parameters.
+ *  numel, grad_dtype, cuda_stream  as for shampoo_clip_create.
+ *  beta1, beta2  decay of the two moments, each in [0, 1).
+ *  epsilon       > 0 (as a float).
+ *  weight_decay  host array [nparams], each >= 0, or NULL for none.
+ *  state_bits    32: both moments in float32.  8: m and r = sqrt(v) as e4m3
+ *                codes, 256 consecutive elements of a tensor to one power of two,
+ *                2^(E - 127) with E one byte: the smallest that brings the
+ *                largest magnitude to 448.  2.008 bytes an element in place of 8.
+ *  max_norm      > 0: every step first clips the list's gradients to this global
+ *                norm (they are not written).  0: no clipping.
+ *  seed          of the 8-bit moments' stochastic rounding.
+ * Moments and step counts start at zero.  Synchronises the stream once.
+ *
+ * The codes are rounded with 16 random bits each from a hash of (seed, step
+ * count, element): m up with the probability of its fraction, r with the one that
+ * keeps the mean of r^2 = v.  Rounded to nearest, v would hardly ever move: with
+ * beta2 = 0.999 it changes by 0.1 % a step, and codes are 6 to 12 % apart.
+ */
+shampoo_status shampoo_adamw_create(shampoo_adamw** out, int nparams, const int64_t* numel,
+                                    double beta1, double beta2, double epsilon,
+                                    const double* weight_decay, int state_bits,
+                                    shampoo_dtype grad_dtype, double max_norm, int64_t seed,
+                                    void* cuda_stream);
+
+/*
+ * shampoo_adamw_step -- one step, per tensor with a finite gradient:
+ *   t <- t + 1
+ *   m <- beta1 m + (1 - beta1) c g,  v <- beta2 v + (1 - beta2) (c g)^2
+ *   W <- W (1 - lr wd) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + epsilon)
+ * with c = max_norm / norm where that clips, else 1.  The step uses m and v as
+ * computed, before they are rounded to codes.  A moment that would pass the largest
+ * float stops there.
+ *  params  host array [nparams] of device float32 pointers, updated in place.
+ *  grads   host array [nparams] of device pointers to elements of grad_dtype.
+ *  copies  host array [nparams] of device bfloat16 pointers that receive the
+ *          updated W rounded to nearest, or NULL.
+ *  lr      learning rate, >= 0.
+ */
+shampoo_status shampoo_adamw_step(shampoo_adamw* adamw, float* const* params,
+                                  const void* const* grads, void* const* copies, double lr);
+
+/*
+ * shampoo_adamw_state -- device address and element count of a part of the state,
+ * to save and restore it (in stream order with the steps).  Library-owned, valid
+ * until shampoo_adamw_destroy.  The moments of all tensors lie in one array each;
+ * tensor i's begin at element shampoo_adamw_offset(i), a multiple of 256, and
+ * what lies between one tensor's end and the next one's beginning is zero and must
+ * stay so.
+ */
+enum {
+  SHAMPOO_ADAMW_NORM = 0,      /* float [1]: the gradient norm of the last step  */
+  SHAMPOO_ADAMW_STEP = 1,      /* int32 [nparams]: t                             */
+  SHAMPOO_ADAMW_M = 2,         /* float32, or e4m3 codes                         */
+  SHAMPOO_ADAMW_V = 3,         /* float32 v, or e4m3 codes of sqrt(v)            */
+  SHAMPOO_ADAMW_M_SCALE = 4,   /* 8 bits only: E, one byte per 256 elements      */
+  SHAMPOO_ADAMW_V_SCALE = 5
+};
+shampoo_status shampoo_adamw_state(shampoo_adamw* adamw, int which, void** data, int64_t* count);
+
+/* First element of tensor `param` in the moments' arrays; -1 for a bad index.  Host value. */
+int64_t shampoo_adamw_offset(const shampoo_adamw* adamw, int param);
+
+/* As shampoo_clip_set_stream. */
+shampoo_status shampoo_adamw_set_stream(shampoo_adamw* adamw, void* cuda_stream);
+
+/* Tensors skipped by the last step because their gradient was not finite.  Synchronises. */
+shampoo_status shampoo_adamw_nonfinite_status(shampoo_adamw* adamw, int* n_params_skipped);
+const char* shampoo_adamw_last_error(const shampoo_adamw* adamw);
+void shampoo_adamw_destroy(shampoo_adamw* adamw);   /* NULL is a no-op */
+
 /* Library version, "MAJOR.MINOR.PATCH". */
 const char* shampoo_version(void);
 

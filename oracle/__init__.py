@@ -1,4 +1,5 @@
-"""fp64 CPU oracle of the Shampoo optimizer step.
+"""fp64 CPU oracle of the Shampoo optimizer step (and, in ``adamw_oracle``, of the
+AdamW step and the gradient clipping).
 
 Test infrastructure only: used by the tests, the smoke check and the bench's
 CPU baseline / reference leg.  The product (``shampoo_second_order_b200``)

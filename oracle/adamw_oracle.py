@@ -1,0 +1,91 @@
+"""fp64 CPU oracle of gradient clipping and the AdamW step, with the moments in
+64 bits or as the 8-bit codes the library defines.  One tensor at a time, from the
+definitions."""
+from __future__ import annotations
+
+import numpy as np
+
+BLOCK = 256
+FLT_MAX = float(np.finfo(np.float32).max)
+
+
+def global_norm(grads):
+    """(norm over the finite gradients, which are finite); grads float64 arrays."""
+    fine = [bool(np.isfinite(g).all()) for g in grads]
+    return float(np.sqrt(sum(float((g * g).sum()) for g, ok in zip(grads, fine) if ok))), fine
+
+
+def clip_factor(norm, max_norm):
+    return max_norm / norm if 0.0 < max_norm < norm else 1.0
+
+
+def adamw(w, g, m, v, t, lr, beta1, beta2, eps, decay):
+    """(w, m, v) after step t (the first is 1) of gradient g."""
+    m = np.clip(beta1 * m + (1.0 - beta1) * g, -FLT_MAX, FLT_MAX)
+    v = np.minimum(beta2 * v + (1.0 - beta2) * g * g, FLT_MAX)
+    d = np.sqrt(v) / np.sqrt(1.0 - beta2 ** t) + eps
+    return w * (1.0 - lr * decay) - lr / (1.0 - beta1 ** t) * m / d, m, v
+
+
+# ---------------- 8-bit moments ----------------
+
+def e4m3_values():
+    """The value of every code byte (NaN for 0x7F and 0xFF)."""
+    c = np.arange(256)
+    e, f = (c >> 3) & 15, c & 7
+    x = np.where(e == 0, f * 2.0 ** -9, (1.0 + f / 8.0) * 2.0 ** (e - 7.0))
+    x[(c & 127) == 127] = np.nan
+    return np.where(c >= 128, -x, x)
+
+
+def rows(x):
+    """A tensor's elements as rows of BLOCK, zeros behind the last."""
+    x = np.asarray(x, dtype=np.float64).ravel()
+    return np.concatenate([x, np.zeros(-len(x) % BLOCK)]).reshape(-1, BLOCK)
+
+
+def scale_bytes(x):
+    """E of each row: the smallest power of two 2^(E - 127) with max|x| <= 448 of it, at least E = 1."""
+    top = np.abs(x).max(axis=1)
+    e = np.full(top.shape, 1)
+    some = top > 0
+    e[some] = np.maximum(np.ceil(np.log2(top[some] / 448.0)).astype(int) + 127, 1)
+    return e
+
+
+def mix32(x):
+    x = np.asarray(x, dtype=np.uint64)
+    for shift, factor in ((16, 0x7FEB352D), (15, 0x846CA68B)):
+        x = (x ^ (x >> np.uint64(shift))) * np.uint64(factor) & np.uint64(0xFFFFFFFF)
+    return x ^ (x >> np.uint64(16))
+
+
+def random_bits(seed, t, first, count):
+    """32 bits for each of `count` elements from element `first` of the flat state on, at step t."""
+    seed &= (1 << 64) - 1
+    key = int(mix32(((seed & 0xFFFFFFFF) + int(mix32(seed >> 32)) + t * 0x632BE5AB) & 0xFFFFFFFF))
+    j = np.arange(first, first + count, dtype=np.uint64)
+    lo, hi = j & np.uint64(0xFFFFFFFF), j >> np.uint64(32)
+    return mix32((lo * np.uint64(0x9E3779B1) + hi * np.uint64(0x85EBCA77) + np.uint64(key)) & np.uint64(0xFFFFFFFF))
+
+
+def round_codes(x, e, bits, square):
+    """Rows x over scales 2^(E - 127) rounded to e4m3 values with 16 random bits an element.
+
+    Returns (values, gap to the next value up, slack): slack is how far, in gaps (for square:
+    as a probability), the element is from where its draw would give another value.  For m that is
+    floor(a / gap + u), which jumps where the sum is a whole number: one jump in this cell between two
+    values, at s = 0 below, and one in either neighbour at a distance of 1.  Likewise for r at p = u."""
+    a = np.abs(x) / 2.0 ** (e[:, None] - 127.0)
+    with np.errstate(divide="ignore"):
+        gap = 2.0 ** (np.maximum(np.floor(np.log2(a)), -6.0) - 3.0)
+    low = np.floor(a / gap) * gap
+    u = bits / 65536.0
+    if square:
+        p = (a * a - low * low) / ((low + gap) ** 2 - low * low)
+        s = p - u
+        up = s > 0
+    else:
+        s = (a - low) / gap + u - 1.0
+        up = s >= 0
+    return np.copysign(low + gap * up, x), gap, np.minimum(np.abs(s), 1.0 - np.abs(s))

@@ -17,6 +17,7 @@ GRAFT_NONE, GRAFT_ADAGRAD = 0, 1
 ROOTS_FP64, ROOTS_INT8_EMULATED = 0, 1
 SIDES_BOTH, SIDE_LEFT, SIDE_RIGHT = 0, 1, 2
 F32, BF16 = 0, 1
+ADAMW_NORM, ADAMW_STEP, ADAMW_M, ADAMW_V, ADAMW_M_SCALE, ADAMW_V_SCALE = range(6)
 
 # name -> (restype, argtypes), exactly the declarations of include/shampoo.h
 _P = C.c_void_p
@@ -56,6 +57,24 @@ SIGNATURES = {
     "shampoo_selftest_stall_next_stats": (C.c_int, [_P]),
     "shampoo_set_gemm_tiles": (C.c_int, [_P, C.c_int]),
     "shampoo_selftest_stall_next_apply": (C.c_int, [_P]),
+    "shampoo_clip_create": (C.c_int, [C.POINTER(_P), C.c_int, C.POINTER(C.c_int64), C.c_int, _P]),
+    "shampoo_clip_norm": (C.c_int, [_P, C.POINTER(_P)]),
+    "shampoo_clip_apply": (C.c_int, [_P, C.POINTER(_P), C.c_double]),
+    "shampoo_clip_result": (C.c_int, [_P, C.POINTER(_P)]),
+    "shampoo_clip_set_stream": (C.c_int, [_P, _P]),
+    "shampoo_clip_nonfinite_status": (C.c_int, [_P, C.POINTER(C.c_int)]),
+    "shampoo_clip_last_error": (C.c_char_p, [_P]),
+    "shampoo_clip_destroy": (None, [_P]),
+    "shampoo_adamw_create": (C.c_int, [C.POINTER(_P), C.c_int, C.POINTER(C.c_int64), C.c_double, C.c_double,
+                                       C.c_double, C.POINTER(C.c_double), C.c_int, C.c_int, C.c_double,
+                                       C.c_int64, _P]),
+    "shampoo_adamw_step": (C.c_int, [_P, C.POINTER(_P), C.POINTER(_P), C.POINTER(_P), C.c_double]),
+    "shampoo_adamw_state": (C.c_int, [_P, C.c_int, C.POINTER(_P), C.POINTER(C.c_int64)]),
+    "shampoo_adamw_offset": (C.c_int64, [_P, C.c_int]),
+    "shampoo_adamw_set_stream": (C.c_int, [_P, _P]),
+    "shampoo_adamw_nonfinite_status": (C.c_int, [_P, C.POINTER(C.c_int)]),
+    "shampoo_adamw_last_error": (C.c_char_p, [_P]),
+    "shampoo_adamw_destroy": (None, [_P]),
     "shampoo_version": (C.c_char_p, []),
 }
 
@@ -263,6 +282,100 @@ def shampoo_selftest_stall_next_stats(ctx):
 
 def shampoo_selftest_stall_next_apply(ctx):
     return _check(lib().shampoo_selftest_stall_next_apply(ctx), ctx)
+
+
+def _check_of(error_of, st, ctx):
+    if st != OK:
+        msg = error_of(ctx)
+        raise ShampooError(st, msg.decode() if msg else "")
+    return st
+
+
+def _counts(numel):
+    return (C.c_int64 * len(numel))(*[int(k) for k in numel])
+
+
+def shampoo_clip_create(numel, grad_dtype=F32, stream=0):
+    """numel: element count of every tensor.  Returns the context handle."""
+    ctx = C.c_void_p()
+    st = lib().shampoo_clip_create(C.byref(ctx), len(numel), _counts(numel), int(grad_dtype),
+                                   C.c_void_p(int(stream)))
+    _check(st, None)
+    return ctx
+
+
+def shampoo_clip_norm(ctx, grads):
+    return _check_of(lib().shampoo_clip_last_error, lib().shampoo_clip_norm(ctx, grads), ctx)
+
+
+def shampoo_clip_apply(ctx, grads, max_norm):
+    return _check_of(lib().shampoo_clip_last_error, lib().shampoo_clip_apply(ctx, grads, float(max_norm)), ctx)
+
+
+def shampoo_clip_result(ctx):
+    """Device address of the last call's norm."""
+    p = C.c_void_p()
+    _check_of(lib().shampoo_clip_last_error, lib().shampoo_clip_result(ctx, C.byref(p)), ctx)
+    return p.value
+
+
+def shampoo_clip_set_stream(ctx, stream):
+    return _check_of(lib().shampoo_clip_last_error,
+                     lib().shampoo_clip_set_stream(ctx, C.c_void_p(int(stream))), ctx)
+
+
+def shampoo_clip_nonfinite_status(ctx):
+    a = C.c_int()
+    _check_of(lib().shampoo_clip_last_error, lib().shampoo_clip_nonfinite_status(ctx, C.byref(a)), ctx)
+    return a.value
+
+
+def shampoo_clip_destroy(ctx):
+    lib().shampoo_clip_destroy(ctx)
+
+
+def shampoo_adamw_create(numel, beta1, beta2, epsilon, weight_decay, state_bits=32, grad_dtype=F32, max_norm=0.0,
+                         seed=0, stream=0):
+    """numel, weight_decay: one value per tensor.  Returns the context handle."""
+    ctx = C.c_void_p()
+    decay = (C.c_double * len(numel))(*[float(d) for d in weight_decay])
+    st = lib().shampoo_adamw_create(C.byref(ctx), len(numel), _counts(numel), float(beta1), float(beta2),
+                                    float(epsilon), decay, int(state_bits), int(grad_dtype), float(max_norm),
+                                    int(seed), C.c_void_p(int(stream)))
+    _check(st, None)
+    return ctx
+
+
+def shampoo_adamw_step(ctx, params, grads, copies, lr):
+    return _check_of(lib().shampoo_adamw_last_error,
+                     lib().shampoo_adamw_step(ctx, params, grads, copies, float(lr)), ctx)
+
+
+def shampoo_adamw_state(ctx, which):
+    """(device address, element count) of a part of the state."""
+    p, n = C.c_void_p(), C.c_int64()
+    _check_of(lib().shampoo_adamw_last_error,
+              lib().shampoo_adamw_state(ctx, int(which), C.byref(p), C.byref(n)), ctx)
+    return p.value, n.value
+
+
+def shampoo_adamw_offset(ctx, param):
+    return lib().shampoo_adamw_offset(ctx, int(param))
+
+
+def shampoo_adamw_set_stream(ctx, stream):
+    return _check_of(lib().shampoo_adamw_last_error,
+                     lib().shampoo_adamw_set_stream(ctx, C.c_void_p(int(stream))), ctx)
+
+
+def shampoo_adamw_nonfinite_status(ctx):
+    a = C.c_int()
+    _check_of(lib().shampoo_adamw_last_error, lib().shampoo_adamw_nonfinite_status(ctx, C.byref(a)), ctx)
+    return a.value
+
+
+def shampoo_adamw_destroy(ctx):
+    lib().shampoo_adamw_destroy(ctx)
 
 
 def shampoo_version():

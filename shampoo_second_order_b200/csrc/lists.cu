@@ -1,0 +1,449 @@
+// Entry points of the many-tensor operators (include/shampoo.h): the clipping of
+// a gradient list to a global norm, and the AdamW step.  A context holds the
+// chunk table of a fixed list of tensors and its state on one device; a call checks the
+// pointers on the host and launches its kernels, nothing else: no copy, no
+// allocation and no wait, so a call can be captured into a graph.
+#include <algorithm>
+#include <cmath>
+#include <memory>
+#include <new>
+#include <string>
+#include <utility>
+#include <vector>
+
+#include "../../include/shampoo.h"
+#include "lists.h"
+
+namespace shampoo {
+void set_global_error(const std::string& msg);   // api.cu
+}  // namespace shampoo
+
+using namespace shampoo;
+
+namespace {
+
+// A run of at most kListGroup tensors and of their chunks: one launch of each kernel.
+struct Group {
+  int p0, np, c0, nc;
+};
+
+// The list itself, common to both contexts.
+struct List {
+  cudaStream_t stream = nullptr;
+  int device = 0;
+  int bf16 = 0;
+  std::vector<int64_t> numel, offset;
+  int64_t total = 0;   // elements of the flat state, the gaps between tensors included
+  std::vector<Group> groups;
+  ListTables tab{};
+  std::vector<void*> allocs;
+  std::string err;
+};
+
+// Makes the list's device current for a call, and the caller's again after it.
+struct OnDevice {
+  int was = -1;
+  explicit OnDevice(int device) {
+    int d = 0;
+    if (cudaGetDevice(&d) == cudaSuccess && d != device && cudaSetDevice(device) == cudaSuccess) was = d;
+  }
+  ~OnDevice() {
+    if (was >= 0) cudaSetDevice(was);
+  }
+};
+
+shampoo_status refuse(List* l, shampoo_status st, const std::string& msg) {
+  if (l) l->err = msg;
+  else set_global_error(msg);
+  return st;
+}
+
+shampoo_status cuda_error(List* l, cudaError_t e, const char* what) {
+  return refuse(l, SHAMPOO_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+// Zeroed device memory, freed with the list.
+template <class T>
+cudaError_t zeroed(List* l, T** p, int64_t count) {
+  void* q = nullptr;
+  cudaError_t e = cudaMalloc(&q, (size_t)count * sizeof(T));
+  if (e != cudaSuccess) {
+    cudaGetLastError();   // reported here; no later launch should find it
+    return e;
+  }
+  l->allocs.push_back(q);
+  *p = static_cast<T*>(q);
+  return cudaMemsetAsync(q, 0, (size_t)count * sizeof(T), l->stream);
+}
+
+void release(List* l) {
+  OnDevice on(l->device);
+  if (!l->allocs.empty()) cudaStreamSynchronize(l->stream);
+  for (void* q : l->allocs) cudaFree(q);
+}
+
+// Checks the list's sizes, then its tables on the host and the device.  The
+// host part comes first: a bad argument touches no GPU.
+shampoo_status check_list(int nparams, const int64_t* numel, int grad_dtype) {
+  if (nparams < 1 || !numel) return refuse(nullptr, SHAMPOO_EINVAL, "need nparams >= 1 and numel");
+  if (grad_dtype != SHAMPOO_F32 && grad_dtype != SHAMPOO_BF16) return refuse(nullptr, SHAMPOO_EINVAL, "unknown grad dtype");
+  int64_t total = 0;
+  for (int i = 0; i < nparams; ++i) {
+    if (numel[i] < 1 || numel[i] > (int64_t(1) << 40))
+      return refuse(nullptr, SHAMPOO_EINVAL, "bad element count for parameter " + std::to_string(i));
+    total += (numel[i] + kListChunk - 1) / kListChunk;
+    if (total > (int64_t(1) << 30)) return refuse(nullptr, SHAMPOO_EINVAL, "more elements than a list can hold");
+  }
+  return SHAMPOO_OK;
+}
+
+shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dtype, void* stream) {
+  l->stream = static_cast<cudaStream_t>(stream);
+  l->bf16 = grad_dtype == SHAMPOO_BF16;
+  cudaError_t e = cudaGetDevice(&l->device);
+  if (e != cudaSuccess) return cuda_error(l, e, "cudaGetDevice");
+  l->numel.assign(numel, numel + nparams);
+  std::vector<ListChunk> chunks;
+  for (int i = 0; i < nparams; ++i) {
+    if (i % kListGroup == 0) l->groups.push_back(Group{i, 0, (int)chunks.size(), 0});
+    l->offset.push_back(l->total);
+    for (int64_t s = 0; s < numel[i]; s += kListChunk) {
+      ListChunk c{};
+      c.param = i;
+      c.len = (int)std::min<int64_t>(kListChunk, numel[i] - s);
+      c.start = s;
+      c.flat = l->total + s;
+      chunks.push_back(c);
+    }
+    l->total += (numel[i] + kQBlock - 1) / kQBlock * kQBlock;
+    Group& g = l->groups.back();
+    g.np = i + 1 - g.p0;
+    g.nc = (int)chunks.size() - g.c0;
+  }
+  l->tab.nchunks = (int)chunks.size();
+  l->tab.nparams = nparams;
+  ListChunk* d = nullptr;
+  if ((e = zeroed(l, &d, l->tab.nchunks)) != cudaSuccess || (e = zeroed(l, &l->tab.partial, l->tab.nchunks)) != cudaSuccess ||
+      (e = zeroed(l, &l->tab.skip, nparams)) != cudaSuccess || (e = zeroed(l, &l->tab.result, 1)) != cudaSuccess)
+    return refuse(l, SHAMPOO_ENOMEM, std::string("device allocation failed: ") + cudaGetErrorString(e));
+  l->tab.chunks = d;
+  // pageable source: staged by the driver before the call returns
+  e = cudaMemcpyAsync(d, chunks.data(), chunks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
+  if (e != cudaSuccess) return cuda_error(l, e, "upload of the chunk table");
+  return SHAMPOO_OK;
+}
+
+// One pointer list of a call: what it is called, its element size, whether the call writes to it.
+struct Ptrs {
+  const char* name;
+  const void* const* p;
+  int size;
+  bool written;
+};
+
+// Every pointer is there and aligned to its element, and nothing that the call
+// writes overlaps anything else that it reads or writes: two CTAs would race.
+shampoo_status check_pointers(List* l, const Ptrs* lists, int count) {
+  struct Run {
+    uintptr_t at, end;
+    int list, param;
+  };
+  const int n = (int)l->numel.size();
+  std::vector<std::vector<Run>> runs(count);
+  for (int k = 0; k < count; ++k) {
+    runs[k].reserve(n);
+    for (int i = 0; i < n; ++i) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(lists[k].p[i]);
+      if (!a) return refuse(l, SHAMPOO_EINVAL, std::string(lists[k].name) + "[" + std::to_string(i) + "] is NULL");
+      if (a % lists[k].size)
+        return refuse(l, SHAMPOO_EINVAL, std::string(lists[k].name) + "[" + std::to_string(i) + "] is not aligned to its elements");
+      runs[k].push_back(Run{a, a + (uintptr_t)l->numel[i] * lists[k].size, k, i});
+    }
+    const auto before = [](const Run& x, const Run& y) { return x.at < y.at; };
+    if (!std::is_sorted(runs[k].begin(), runs[k].end(), before)) std::sort(runs[k].begin(), runs[k].end(), before);
+  }
+  // merge the sorted lists, with the furthest end of what was written and of all
+  std::vector<size_t> next(count, 0);
+  Run any{0, 0, 0, 0}, written{0, 0, 0, 0};
+  for (;;) {
+    int k = -1;
+    for (int j = 0; j < count; ++j)
+      if (next[j] < runs[j].size() && (k < 0 || runs[j][next[j]].at < runs[k][next[k]].at)) k = j;
+    if (k < 0) return SHAMPOO_OK;
+    const Run r = runs[k][next[k]++];
+    const Run& hit = lists[k].written ? any : written;
+    if (r.at < hit.end)
+      return refuse(l, SHAMPOO_EINVAL, std::string(lists[k].name) + "[" + std::to_string(r.param) + "] overlaps " +
+                                           lists[hit.list].name + "[" + std::to_string(hit.param) + "]");
+    if (r.end > any.end) any = r;
+    if (lists[k].written && r.end > written.end) written = r;
+  }
+}
+
+shampoo_status read_skipped(List* l, int* n) {
+  if (!n) return refuse(l, SHAMPOO_EINVAL, "n_params_skipped is NULL");
+  OnDevice on(l->device);
+  ListResult r{};
+  cudaError_t e = cudaMemcpyAsync(&r, l->tab.result, sizeof(r), cudaMemcpyDeviceToHost, l->stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(l->stream);
+  if (e != cudaSuccess) return cuda_error(l, e, "nonfinite_status");
+  *n = r.skipped;
+  return SHAMPOO_OK;
+}
+
+// std::bad_alloc and the like must not leave a C entry point.
+template <class F>
+shampoo_status guarded(List* l, F&& f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return l ? SHAMPOO_ENOMEM : refuse(nullptr, SHAMPOO_ENOMEM, "out of host memory");
+  } catch (...) {
+    return SHAMPOO_ECUDA;
+  }
+}
+
+}  // namespace
+
+struct shampoo_clip {
+  List list;
+};
+
+struct shampoo_adamw {
+  List list;
+  int bits = 32;
+  double beta1 = 0.9, beta2 = 0.999, eps = 1e-8, max_norm = 0.0;
+  uint64_t seed = 0;
+  AdamwState st{};
+  int* step = nullptr;
+  ListStep* factors = nullptr;
+  double* decay = nullptr;
+};
+
+extern "C" {
+
+// ---------------- gradient clipping ----------------
+
+shampoo_status shampoo_clip_create(shampoo_clip** out, int nparams, const int64_t* numel, shampoo_dtype grad_dtype,
+                                   void* cuda_stream) {
+  if (!out) return refuse(nullptr, SHAMPOO_EINVAL, "out is NULL");
+  *out = nullptr;
+  return guarded(nullptr, [&] {
+    shampoo_status st = check_list(nparams, numel, grad_dtype);
+    if (st != SHAMPOO_OK) return st;
+    std::unique_ptr<shampoo_clip, void (*)(shampoo_clip*)> c(new shampoo_clip(), shampoo_clip_destroy);
+    st = make_list(&c->list, nparams, numel, grad_dtype, cuda_stream);
+    if (st == SHAMPOO_OK) {
+      const cudaError_t e = cudaStreamSynchronize(c->list.stream);
+      if (e != cudaSuccess) st = cuda_error(&c->list, e, "set-up");
+    }
+    if (st != SHAMPOO_OK) {
+      set_global_error(c->list.err);
+      return st;
+    }
+    *out = c.release();
+    return SHAMPOO_OK;
+  });
+}
+
+shampoo_status shampoo_clip_norm(shampoo_clip* clip, const void* const* grads) {
+  if (!clip) return refuse(nullptr, SHAMPOO_EINVAL, "clip is NULL");
+  List* l = &clip->list;
+  if (!grads) return refuse(l, SHAMPOO_EINVAL, "grads is NULL");
+  return guarded(l, [&] {
+    const Ptrs lists[] = {{"grads", grads, l->bf16 ? 2 : 4, false}};
+    const shampoo_status st = check_pointers(l, lists, 1);
+    if (st != SHAMPOO_OK) return st;
+    OnDevice on(l->device);
+    for (const Group& g : l->groups) {
+      const cudaError_t e = launch_list_norm(l->tab, grads, g.p0, g.np, g.c0, g.nc, l->bf16, 0.0, ListAdvance{}, l->stream);
+      if (e != cudaSuccess) return cuda_error(l, e, "list_norm");
+    }
+    return SHAMPOO_OK;
+  });
+}
+
+shampoo_status shampoo_clip_apply(shampoo_clip* clip, void* const* grads, double max_norm) {
+  if (!clip) return refuse(nullptr, SHAMPOO_EINVAL, "clip is NULL");
+  List* l = &clip->list;
+  if (!grads) return refuse(l, SHAMPOO_EINVAL, "grads is NULL");
+  if (!(max_norm > 0.0) || !std::isfinite(max_norm)) return refuse(l, SHAMPOO_EINVAL, "max_norm must be > 0");
+  return guarded(l, [&] {
+    const void* const* g0 = const_cast<const void* const*>(grads);
+    const Ptrs lists[] = {{"grads", g0, l->bf16 ? 2 : 4, true}};
+    const shampoo_status st = check_pointers(l, lists, 1);
+    if (st != SHAMPOO_OK) return st;
+    OnDevice on(l->device);
+    cudaError_t e = cudaSuccess;
+    for (const Group& g : l->groups)
+      if ((e = launch_list_norm(l->tab, g0, g.p0, g.np, g.c0, g.nc, l->bf16, max_norm, ListAdvance{}, l->stream)) != cudaSuccess)
+        return cuda_error(l, e, "list_norm");
+    for (const Group& g : l->groups)
+      if ((e = launch_list_scale(l->tab, grads, g.p0, g.np, g.c0, g.nc, l->bf16, l->stream)) != cudaSuccess)
+        return cuda_error(l, e, "list_scale");
+    return SHAMPOO_OK;
+  });
+}
+
+shampoo_status shampoo_clip_result(shampoo_clip* clip, void** norm) {
+  if (!clip) return refuse(nullptr, SHAMPOO_EINVAL, "clip is NULL");
+  if (!norm) return refuse(&clip->list, SHAMPOO_EINVAL, "norm is NULL");
+  *norm = &clip->list.tab.result->norm;
+  return SHAMPOO_OK;
+}
+
+shampoo_status shampoo_clip_set_stream(shampoo_clip* clip, void* cuda_stream) {
+  if (!clip) return refuse(nullptr, SHAMPOO_EINVAL, "clip is NULL");
+  clip->list.stream = static_cast<cudaStream_t>(cuda_stream);
+  return SHAMPOO_OK;
+}
+
+shampoo_status shampoo_clip_nonfinite_status(shampoo_clip* clip, int* n_params_skipped) {
+  if (!clip) return refuse(nullptr, SHAMPOO_EINVAL, "clip is NULL");
+  return read_skipped(&clip->list, n_params_skipped);
+}
+
+const char* shampoo_clip_last_error(const shampoo_clip* clip) {
+  return clip ? clip->list.err.c_str() : shampoo_last_error(nullptr);
+}
+
+void shampoo_clip_destroy(shampoo_clip* clip) {
+  if (!clip) return;
+  release(&clip->list);
+  delete clip;
+}
+
+// ---------------- AdamW ----------------
+
+shampoo_status shampoo_adamw_create(shampoo_adamw** out, int nparams, const int64_t* numel, double beta1, double beta2,
+                                    double epsilon, const double* weight_decay, int state_bits, shampoo_dtype grad_dtype,
+                                    double max_norm, int64_t seed, void* cuda_stream) {
+  if (!out) return refuse(nullptr, SHAMPOO_EINVAL, "out is NULL");
+  *out = nullptr;
+  return guarded(nullptr, [&] {
+    shampoo_status st = check_list(nparams, numel, grad_dtype);
+    if (st != SHAMPOO_OK) return st;
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
+      return refuse(nullptr, SHAMPOO_EINVAL, "beta1 and beta2 must be in [0, 1)");
+    // held in 32 bits on the device: a denominator of zero would follow from one that rounds to it
+    if (!((float)epsilon > 0.f) || !std::isfinite((float)epsilon)) return refuse(nullptr, SHAMPOO_EINVAL, "epsilon must be > 0");
+    if (state_bits != 32 && state_bits != 8) return refuse(nullptr, SHAMPOO_EINVAL, "state_bits must be 32 or 8");
+    if (!(max_norm >= 0.0) || !std::isfinite(max_norm)) return refuse(nullptr, SHAMPOO_EINVAL, "max_norm must be >= 0 (0: no clipping)");
+    for (int i = 0; weight_decay && i < nparams; ++i)
+      if (!(weight_decay[i] >= 0.0) || !std::isfinite(weight_decay[i]))
+        return refuse(nullptr, SHAMPOO_EINVAL, "weight_decay must be >= 0");
+    std::unique_ptr<shampoo_adamw, void (*)(shampoo_adamw*)> a(new shampoo_adamw(), shampoo_adamw_destroy);
+    List* l = &a->list;
+    a->bits = state_bits;
+    a->beta1 = beta1;
+    a->beta2 = beta2;
+    a->eps = epsilon;
+    a->max_norm = max_norm;
+    a->seed = (uint64_t)seed;
+    st = make_list(l, nparams, numel, grad_dtype, cuda_stream);
+    if (st == SHAMPOO_OK) {
+      cudaError_t e = zeroed(l, &a->step, nparams);
+      if (e == cudaSuccess) e = zeroed(l, &a->factors, nparams);
+      if (e == cudaSuccess) e = zeroed(l, &a->decay, nparams);
+      if (state_bits == 32) {
+        if (e == cudaSuccess) e = zeroed(l, &a->st.m, l->total);
+        if (e == cudaSuccess) e = zeroed(l, &a->st.v, l->total);
+      } else {
+        if (e == cudaSuccess) e = zeroed(l, &a->st.mq, l->total);
+        if (e == cudaSuccess) e = zeroed(l, &a->st.rq, l->total);
+        if (e == cudaSuccess) e = zeroed(l, &a->st.ms, l->total / kQBlock);
+        if (e == cudaSuccess) e = zeroed(l, &a->st.rs, l->total / kQBlock);
+      }
+      if (e != cudaSuccess) st = refuse(l, SHAMPOO_ENOMEM, std::string("device allocation failed: ") + cudaGetErrorString(e));
+    }
+    if (st == SHAMPOO_OK) {
+      cudaError_t e = cudaSuccess;
+      if (weight_decay)
+        e = cudaMemcpyAsync(a->decay, weight_decay, nparams * sizeof(double), cudaMemcpyHostToDevice, l->stream);
+      if (e == cudaSuccess) e = cudaStreamSynchronize(l->stream);
+      if (e != cudaSuccess) st = cuda_error(l, e, "set-up");
+    }
+    if (st != SHAMPOO_OK) {
+      set_global_error(l->err);
+      return st;
+    }
+    *out = a.release();
+    return SHAMPOO_OK;
+  });
+}
+
+shampoo_status shampoo_adamw_step(shampoo_adamw* adamw, float* const* params, const void* const* grads, void* const* copies,
+                                  double lr) {
+  if (!adamw) return refuse(nullptr, SHAMPOO_EINVAL, "adamw is NULL");
+  shampoo_adamw* a = adamw;
+  List* l = &a->list;
+  if (!params || !grads) return refuse(l, SHAMPOO_EINVAL, "params or grads is NULL");
+  if (!(lr >= 0.0) || !std::isfinite(lr)) return refuse(l, SHAMPOO_EINVAL, "lr must be >= 0");
+  return guarded(l, [&] {
+    const Ptrs lists[] = {{"params", reinterpret_cast<const void* const*>(params), 4, true},
+                          {"grads", grads, l->bf16 ? 2 : 4, false},
+                          {"copies", const_cast<const void* const*>(copies), 2, true}};
+    const shampoo_status st = check_pointers(l, lists, copies ? 3 : 2);
+    if (st != SHAMPOO_OK) return st;
+    OnDevice on(l->device);
+    const ListAdvance adv{a->step, a->factors, a->decay, lr, a->beta1, a->beta2, (uint32_t)a->seed, (uint32_t)(a->seed >> 32)};
+    cudaError_t e = cudaSuccess;
+    for (const Group& g : l->groups)
+      if ((e = launch_list_norm(l->tab, grads, g.p0, g.np, g.c0, g.nc, l->bf16, a->max_norm, adv, l->stream)) != cudaSuccess)
+        return cuda_error(l, e, "list_norm");
+    for (const Group& g : l->groups)
+      if ((e = launch_adamw(l->tab, params, grads, copies, g.p0, g.np, g.c0, g.nc, l->bf16, a->bits == 8, a->st, a->factors,
+                            (float)a->beta1, (float)(1.0 - a->beta1), (float)a->beta2, (float)(1.0 - a->beta2), (float)a->eps,
+                            l->stream)) != cudaSuccess)
+        return cuda_error(l, e, "adamw");
+    return SHAMPOO_OK;
+  });
+}
+
+shampoo_status shampoo_adamw_state(shampoo_adamw* adamw, int which, void** data, int64_t* count) {
+  if (!adamw) return refuse(nullptr, SHAMPOO_EINVAL, "adamw is NULL");
+  const List* l = &adamw->list;
+  const bool eight = adamw->bits == 8;
+  void* p = nullptr;
+  int64_t n = l->total;
+  switch (which) {
+    case SHAMPOO_ADAMW_NORM: p = &l->tab.result->norm; n = 1; break;
+    case SHAMPOO_ADAMW_STEP: p = adamw->step; n = (int64_t)l->numel.size(); break;
+    case SHAMPOO_ADAMW_M: p = eight ? (void*)adamw->st.mq : adamw->st.m; break;
+    case SHAMPOO_ADAMW_V: p = eight ? (void*)adamw->st.rq : adamw->st.v; break;
+    case SHAMPOO_ADAMW_M_SCALE: p = adamw->st.ms; n /= kQBlock; break;
+    case SHAMPOO_ADAMW_V_SCALE: p = adamw->st.rs; n /= kQBlock; break;
+  }
+  if (!p || !data || !count) return refuse(&adamw->list, SHAMPOO_EINVAL, "bad which, or data or count is NULL");
+  *data = p;
+  *count = n;
+  return SHAMPOO_OK;
+}
+
+int64_t shampoo_adamw_offset(const shampoo_adamw* adamw, int param) {
+  if (!adamw || param < 0 || param >= (int)adamw->list.offset.size()) return -1;
+  return adamw->list.offset[param];
+}
+
+shampoo_status shampoo_adamw_set_stream(shampoo_adamw* adamw, void* cuda_stream) {
+  if (!adamw) return refuse(nullptr, SHAMPOO_EINVAL, "adamw is NULL");
+  adamw->list.stream = static_cast<cudaStream_t>(cuda_stream);
+  return SHAMPOO_OK;
+}
+
+shampoo_status shampoo_adamw_nonfinite_status(shampoo_adamw* adamw, int* n_params_skipped) {
+  if (!adamw) return refuse(nullptr, SHAMPOO_EINVAL, "adamw is NULL");
+  return read_skipped(&adamw->list, n_params_skipped);
+}
+
+const char* shampoo_adamw_last_error(const shampoo_adamw* adamw) {
+  return adamw ? adamw->list.err.c_str() : shampoo_last_error(nullptr);
+}
+
+void shampoo_adamw_destroy(shampoo_adamw* adamw) {
+  if (!adamw) return;
+  release(&adamw->list);
+  delete adamw;
+}
+
+}  // extern "C"

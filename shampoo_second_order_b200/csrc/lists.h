@@ -1,0 +1,74 @@
+// Many-tensor operators over a fixed list of tensors: declarations shared by
+// the kernels (k_adamw.cu) and the entry points (lists.cu).
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace shampoo {
+
+constexpr int kListChunk = 8192;   // elements per CTA of the list kernels
+constexpr int kQBlock = 256;       // elements per scale of the 8-bit moments; every
+                                   // tensor's state starts at a multiple of it
+
+// A contiguous run of one tensor's elements, at most kListChunk of them.
+struct ListChunk {
+  int param;
+  int len;
+  int64_t start;   // first element inside the tensor, a multiple of kListChunk
+  int64_t flat;    // first element in the flat state, a multiple of kQBlock
+};
+
+// What one pass over the gradients leaves for the kernels after it.
+struct ListResult {
+  float norm;       // over the tensors whose gradient is finite
+  float coef;       // the clipping factor, 1 without clipping
+  int skipped;      // tensors whose gradient is not finite
+  unsigned done;    // CTAs of the pass that have finished (zero between passes)
+};
+
+// Per-tensor factors of one AdamW step.
+struct ListStep {
+  float first;      // lr / (1 - b1^t)
+  float second;     // 1 / sqrt(1 - b2^t)
+  float shrink;     // 1 - lr wd
+  uint32_t key;     // of the stochastic rounding's hash
+};
+
+// AdamW's part of the pass's end: advance t and set ListStep (null step: none).
+struct ListAdvance {
+  int* step;              // [n] t of each tensor
+  ListStep* out;          // [n]
+  const double* decay;    // [n]
+  double lr, beta1, beta2;
+  uint32_t seed_lo, seed_hi;
+};
+
+// The tables of a pass over the gradients.
+struct ListTables {
+  const ListChunk* chunks;
+  double* partial;        // [nchunks] sum of squares, NaN where an element is not finite
+  int* skip;              // [n] 1: the tensor's gradient is not finite
+  ListResult* result;
+  int nchunks, nparams;
+};
+
+// Tensor pointers travel as kernel arguments, so that a captured launch keeps
+// its own and nothing is copied to the device: at most kListGroup a launch.
+constexpr int kListGroup = 1024;
+
+struct AdamwState {
+  float *m, *v;                 // 32-bit moments
+  uint8_t *mq, *rq, *ms, *rs;   // 8-bit: codes of m and sqrt(v), scale exponents
+};
+
+// The norm of the tensors [p0, p0 + np), whose chunks are [c0, c0 + nc); the launch
+// that finishes last closes the pass over all chunks.
+cudaError_t launch_list_norm(const ListTables& t, const void* const* g, int p0, int np, int c0, int nc, int bf16,
+                             double max_norm, const ListAdvance& adv, cudaStream_t s);
+cudaError_t launch_list_scale(const ListTables& t, void* const* g, int p0, int np, int c0, int nc, int bf16,
+                              cudaStream_t s);
+cudaError_t launch_adamw(const ListTables& t, float* const* w, const void* const* g, void* const* copies, int p0,
+                         int np, int c0, int nc, int bf16, int eight, const AdamwState& st, const ListStep* step,
+                         float beta1, float omb1, float beta2, float omb2, float eps, cudaStream_t s);
+
+}  // namespace shampoo

@@ -1,0 +1,205 @@
+"""Torch-facing handles of the many-tensor operators in include/shampoo.h: the
+clipping of a gradient list to a global norm, and the AdamW step.  All
+arithmetic runs in the CUDA library."""
+from __future__ import annotations
+
+import ctypes as C
+from array import array
+from math import prod
+
+from . import _lib as L
+
+
+class _Handle:
+    """A library context, destroyed with its last holder: the tensors that view its
+    memory hold it too."""
+
+    def __init__(self, ctx, destroy):
+        self.ctx, self._destroy = ctx, destroy
+
+    def __del__(self):
+        try:
+            self._destroy(self.ctx)
+        except Exception:
+            pass
+
+
+class _Memory:
+    """Library-owned device memory, for torch.as_tensor to view."""
+
+    def __init__(self, handle, address, count, typestr):
+        self._handle = handle
+        self.__cuda_array_interface__ = {"shape": (count,), "typestr": typestr, "data": (address, False),
+                                         "version": 3, "strides": None}
+
+
+class _List:
+    """A fixed list of tensors on one device.  Work is queued on the current stream of each
+    call, or, where a stream is given, on that one: then the call's work follows what
+    the current stream holds so far, and the current stream waits for it."""
+
+    def __init__(self, shapes, grad_dtype, stream):
+        import torch
+        if grad_dtype not in ("f32", "bf16"):
+            raise ValueError('grad_dtype must be "f32" or "bf16"')
+        self.shapes = [tuple(int(d) for d in s) for s in shapes]
+        self._numel = [prod(s) for s in self.shapes]   # checked on every call
+        self.grad_dtype = torch.bfloat16 if grad_dtype == "bf16" else torch.float32
+        self._grad_code = L.BF16 if grad_dtype == "bf16" else L.F32
+        # without a stream of its own the context follows the caller's current one
+        self._follows = stream is None
+        if stream is None:
+            stream = torch.cuda.current_stream()
+        elif not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream))
+        self.stream = stream
+        self._device = stream.device_index
+        self._handle = self._norm = self._state = None
+
+    def _pointers(self, ts, what, dtype):
+        """The C array of a list's device pointers, after its checks."""
+        from torch import Tensor
+        ts = list(ts)
+        if len(ts) != len(self._numel):
+            raise ValueError(f"expected {len(self._numel)} {what}, got {len(ts)}")
+        if list(map(Tensor.numel, ts)) != self._numel or not all(map(Tensor.is_contiguous, ts)) \
+                or any(t.dtype is not dtype for t in ts) or set(map(Tensor.get_device, ts)) != {self._device}:
+            raise ValueError(f"{what} must be contiguous {dtype} tensors of the given shapes "
+                             f"on CUDA device {self._device}")
+        return (C.c_void_p * len(ts)).from_buffer(array("Q", map(Tensor.data_ptr, ts)))
+
+    def _on_stream(self, set_stream, call):
+        """Run `call` in the order of the caller's current stream."""
+        import torch
+        current = torch.cuda.current_stream(self._device)
+        if current.cuda_stream == self.stream.cuda_stream:
+            call()
+        elif not self._follows:
+            self.stream.wait_stream(current)
+            call()
+            current.wait_stream(self.stream)
+        elif torch.cuda.is_current_stream_capturing():
+            # a graph's place among the context's other calls is that of its replays
+            set_stream(self._ctx, current.cuda_stream)
+            try:
+                call()
+            finally:
+                set_stream(self._ctx, self.stream.cuda_stream)
+        else:
+            current.wait_stream(self.stream)   # the context's earlier calls
+            set_stream(self._ctx, current.cuda_stream)
+            self.stream = current
+            call()
+
+    def _view(self, address, count, typestr):
+        import torch
+        return torch.as_tensor(_Memory(self._handle, address, count, typestr), device=f"cuda:{self._device}")
+
+    @property
+    def _ctx(self):
+        if self._handle is None:
+            raise RuntimeError("the context is closed")
+        return self._handle.ctx
+
+    def close(self):
+        """Give the context up.  Its memory is freed once no tensor views it."""
+        self._handle = self._norm = self._state = None
+
+
+class GradClip(_List):
+    """Global norm and clipping of gradient lists of fixed shapes.
+
+    Gradients are contiguous float32 or bfloat16 CUDA tensors (grad_dtype "f32" /
+    "bf16").  One that holds a NaN or Inf does not count and is not scaled."""
+
+    def __init__(self, shapes, grad_dtype="f32", stream=None):
+        super().__init__(shapes, grad_dtype, stream)
+        self._handle = _Handle(L.shampoo_clip_create(self._numel, self._grad_code, self.stream.cuda_stream),
+                               L.shampoo_clip_destroy)
+        self._norm = self._view(L.shampoo_clip_result(self._ctx), 1, "<f4")[0]
+
+    def norm(self, grads):
+        """The global norm, as a 0-d CUDA tensor that the next call overwrites."""
+        ctx, p = self._ctx, self._pointers(grads, "grads", self.grad_dtype)
+        self._on_stream(L.shampoo_clip_set_stream, lambda: L.shampoo_clip_norm(ctx, p))
+        return self._norm
+
+    def clip(self, grads, max_norm):
+        """Scale the gradients in place to a global norm of at most max_norm.
+        Returns the norm they had, as norm() does."""
+        ctx, p = self._ctx, self._pointers(grads, "grads", self.grad_dtype)
+        self._on_stream(L.shampoo_clip_set_stream, lambda: L.shampoo_clip_apply(ctx, p, max_norm))
+        return self._norm
+
+    def nonfinite_status(self):
+        """Gradients that the last call skipped.  Synchronises."""
+        return L.shampoo_clip_nonfinite_status(self._ctx)
+
+
+class AdamW(_List):
+    """AdamW for a fixed list of float32 parameters.
+
+    shapes: of the parameters.  weight_decay: one value, or one per parameter.
+    state: "f32", or "8bit" for moments of two bytes an element.  max_norm: clip the
+    list's gradients to this global norm in every step (0: don't).  seed: of
+    the 8-bit moments' stochastic rounding.  Gradients are float32 or bfloat16 CUDA
+    tensors (grad_dtype "f32" / "bf16"); all tensors are contiguous.  A parameter
+    whose gradient holds a NaN or Inf is skipped for the step.
+    """
+
+    def __init__(self, shapes, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, state="f32", grad_dtype="f32",
+                 max_norm=0.0, seed=0, stream=None):
+        super().__init__(shapes, grad_dtype, stream)
+        if state not in ("f32", "8bit"):
+            raise ValueError('state must be "f32" or "8bit"')
+        self.state = state
+        decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * len(self.shapes)
+        if len(decay) != len(self.shapes):
+            raise ValueError(f"expected {len(self.shapes)} values of weight_decay, got {len(decay)}")
+        ctx = L.shampoo_adamw_create(self._numel, beta1, beta2, eps, decay, 8 if state == "8bit" else 32,
+                                     self._grad_code, max_norm, seed, self.stream.cuda_stream)
+        self._handle = _Handle(ctx, L.shampoo_adamw_destroy)
+        self.offsets = [L.shampoo_adamw_offset(ctx, i) for i in range(len(self.shapes))]
+        self._norm = self._part(L.ADAMW_NORM, "<f4")[0]
+        self._state = self._views()
+
+    def _part(self, which, typestr):
+        return self._view(*L.shampoo_adamw_state(self._ctx, which), typestr)
+
+    def _views(self):
+        import torch
+        step = self._part(L.ADAMW_STEP, "<i4")
+        if self.state == "f32":
+            return {"step": step, "m": self._part(L.ADAMW_M, "<f4"), "v": self._part(L.ADAMW_V, "<f4")}
+        f8, e8 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+        return {"step": step,
+                "m": self._part(L.ADAMW_M, "|u1").view(f8), "m_scale": self._part(L.ADAMW_M_SCALE, "|u1").view(e8),
+                "r": self._part(L.ADAMW_V, "|u1").view(f8), "r_scale": self._part(L.ADAMW_V_SCALE, "|u1").view(e8)}
+
+    def state_tensors(self):
+        """The state as tensors over the library's memory, to save, and to restore by
+        copying into them: step counts, and the moments of all parameters in
+        one array each, parameter i's from element offsets[i] on (zeros in
+        between).  "f32": m and v.  "8bit": m and r = sqrt(v) in float8, each times
+        one of m_scale / r_scale per 256 elements."""
+        if self._state is None:
+            raise RuntimeError("the context is closed")
+        return dict(self._state)
+
+    def step(self, params, grads, lr, copies=None):
+        """One step.  copies: bfloat16 tensors that receive the updated parameters."""
+        import torch
+        ctx = self._ctx
+        w = self._pointers(params, "params", torch.float32)
+        g = self._pointers(grads, "grads", self.grad_dtype)
+        b = None if copies is None else self._pointers(copies, "copies", torch.bfloat16)
+        self._on_stream(L.shampoo_adamw_set_stream, lambda: L.shampoo_adamw_step(ctx, w, g, b, lr))
+
+    def grad_norm(self):
+        """The gradient norm of the last step before clipping, as a 0-d CUDA tensor
+        that the next step overwrites."""
+        return self._norm
+
+    def nonfinite_status(self):
+        """Parameters that the last step skipped.  Synchronises."""
+        return L.shampoo_adamw_nonfinite_status(self._ctx)
