@@ -535,7 +535,7 @@ void shampoo_clip_destroy(shampoo_clip* clip);   /* NULL is a no-op */
  * shampoo_adamw_create -- AdamW over `nparams` float32 parameters.
  *  numel, grad_dtype, cuda_stream  as for shampoo_clip_create.
  *  beta1, beta2  decay of the two moments, each in [0, 1).
- *  epsilon       > 0 (as a float).
+ *  epsilon       at least FLT_MIN, 1.18e-38 (the step divides by it where v is 0).
  *  weight_decay  host array [nparams], each >= 0, or NULL for none.
  *  state_bits    32: both moments in float32.  8: m and r = sqrt(v) as e4m3
  *                codes, 256 consecutive elements of a tensor to one power of two,
@@ -563,8 +563,8 @@ shampoo_status shampoo_adamw_create(shampoo_adamw** out, int nparams, const int6
  *   m <- beta1 m + (1 - beta1) c g,  v <- beta2 v + (1 - beta2) (c g)^2
  *   W <- W (1 - lr wd) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + epsilon)
  * with c = max_norm / norm where that clips, else 1.  The step uses m and v as
- * computed, before they are rounded to codes.  A moment that would pass the largest
- * float stops there.
+ * computed, before they are rounded to codes.  An element of c g beyond 2^63 in
+ * magnitude counts as 2^63: its square would pass the largest float.
  *  params  host array [nparams] of device float32 pointers, updated in place.
  *  grads   host array [nparams] of device pointers to elements of grad_dtype.
  *  copies  host array [nparams] of device bfloat16 pointers that receive the

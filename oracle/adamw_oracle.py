@@ -6,7 +6,6 @@ from __future__ import annotations
 import numpy as np
 
 BLOCK = 256
-FLT_MAX = float(np.finfo(np.float32).max)
 
 
 def global_norm(grads):
@@ -20,9 +19,10 @@ def clip_factor(norm, max_norm):
 
 
 def adamw(w, g, m, v, t, lr, beta1, beta2, eps, decay):
-    """(w, m, v) after step t (the first is 1) of gradient g."""
-    m = np.clip(beta1 * m + (1.0 - beta1) * g, -FLT_MAX, FLT_MAX)
-    v = np.minimum(beta2 * v + (1.0 - beta2) * g * g, FLT_MAX)
+    """(w, m, v) after step t (the first is 1) of gradient g, whose elements count as at most 2^63."""
+    g = np.clip(g, -2.0 ** 63, 2.0 ** 63)
+    m = beta1 * m + (1.0 - beta1) * g
+    v = beta2 * v + (1.0 - beta2) * g * g
     d = np.sqrt(v) / np.sqrt(1.0 - beta2 ** t) + eps
     return w * (1.0 - lr * decay) - lr / (1.0 - beta1 ** t) * m / d, m, v
 

@@ -21,7 +21,9 @@ namespace shampoo {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 32 * kListWarps;
+constexpr int kSms = 148;
+constexpr float kGradMax = 0x1p63f;   // an element beyond counts as this: its square would pass the largest float
 
 template <int K>
 struct Pointers {
@@ -73,28 +75,6 @@ __device__ __forceinline__ void store4(void* p, int64_t i, const float (&x)[4]) 
   }
 }
 
-// Elements [i, i + 4) of a run of len, zeros behind its end.
-template <bool BF16>
-__device__ __forceinline__ void load4_any(const void* p, int64_t base, int i, int len, bool aligned, float (&x)[4]) {
-  if (aligned && i + 4 <= len) {
-    load4<BF16>(p, base + i, x);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) x[q] = i + q < len ? load1<BF16>(p, base + i + q) : 0.0f;
-  }
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store4_any(void* p, int64_t base, int i, int len, bool aligned, const float (&x)[4]) {
-  if (aligned && i + 4 <= len) {
-    store4<BF16>(p, base + i, x);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (i + q < len) store1<BF16>(p, base + i + q, x[q]);
-  }
-}
-
 // Chunks start at multiples of kListChunk, so the tensor's own address decides.
 template <bool BF16>
 __device__ __forceinline__ bool aligned4(const void* p) {
@@ -109,40 +89,78 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// Closes the pass over the gradients: which tensors are skipped, the norm over
-// the others, the clipping factor and, for AdamW, each tensor's t and factors.
-// One CTA, fixed order: the same gradients give the same bits.
-__device__ void close_pass(const ListTables& t, double max_norm, const ListAdvance& adv, double* red) {
-  int* skip = t.skip;
-  for (int p = threadIdx.x; p < t.nparams; p += blockDim.x) skip[p] = 0;
-  __syncthreads();
-  for (int c = threadIdx.x; c < t.nchunks; c += blockDim.x)
-    if (isnan(__ldcg(&t.partial[c]))) skip[t.chunks[c].param] = 1;
-  __syncthreads();
-  double sum = 0.0;
-  for (int c = threadIdx.x; c < t.nchunks; c += blockDim.x) {
-    const double x = __ldcg(&t.partial[c]);
-    if (!skip[t.chunks[c].param]) sum += x;
+// A run of elements as 16-byte vectors, with up to E - 1 single elements before
+// and behind them: the gradient pass needs no alignment of the tensor.
+template <bool BF16>
+struct Vectors {
+  static constexpr int E = BF16 ? 8 : 4;                      // elements of a vector
+  static constexpr int N = kListChunk / E / kThreads;         // vectors a thread
+  static constexpr int SIZE = BF16 ? 2 : 4;
+  int head, nvec, tail;
+  char* base;      // of the first vector
+  __device__ __forceinline__ Vectors(const void* p, int64_t start, int len) {
+    char* a = static_cast<char*>(const_cast<void*>(p)) + start * SIZE;
+    head = min((int)((16 - (reinterpret_cast<uintptr_t>(a) & 15)) & 15) / SIZE, len);
+    nvec = (len - head) / E;
+    tail = len - head - nvec * E;
+    base = a + head * SIZE;
   }
-  sum = block_sum(sum, red);
-  int skipped = 0;
-  for (int p = threadIdx.x; p < t.nparams; p += blockDim.x) {
-    const int sk = skip[p];
-    skipped += sk;
-    if (adv.step) {
-      const int n = adv.step[p] + (sk ? 0 : 1);
-      adv.step[p] = n;
-      if (!sk) {
-        ListStep o;
-        // 1 - b^t loses digits where t is small: in 64 bits, rounded once
-        o.first = (float)(adv.lr / (1.0 - pow(adv.beta1, (double)n)));
-        o.second = (float)(1.0 / sqrt(1.0 - pow(adv.beta2, (double)n)));
-        o.shrink = (float)(1.0 - adv.lr * adv.decay[p]);
-        o.key = mix32(adv.seed_lo + mix32(adv.seed_hi) + (uint32_t)n * 0x632BE5ABu);
-        adv.out[p] = o;
-      }
+  __device__ __forceinline__ uint4* at(int v) const { return reinterpret_cast<uint4*>(base) + v; }
+  // the single element of this thread, if any: threads 0.. take the head, 32.. the tail
+  __device__ __forceinline__ void* single() const {
+    const int t = threadIdx.x;
+    if (t < head) return base + (t - head) * SIZE;
+    if (t >= 32 && t - 32 < tail) return base + (int64_t)nvec * 16 + (t - 32) * SIZE;
+    return nullptr;
+  }
+};
+
+template <bool BF16>
+__device__ __forceinline__ void widen(const uint4& u, float* x) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if (BF16) {
+      x[2 * q] = __uint_as_float(w[q] << 16);
+      x[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+    } else {
+      x[q] = __uint_as_float(w[q]);
     }
   }
+}
+
+// One tensor's factors of the step that it takes if its gradient is finite.
+// 1 - b^t loses digits where t is small: in 64 bits, rounded once.
+__device__ void step_factors(const ListAdvance& adv, int p) {
+  const int n = adv.step[p] + 1;
+  ListStep o;
+  o.first = (float)(adv.lr / (1.0 - pow(adv.beta1, (double)n)));
+  o.second = (float)(1.0 / sqrt(1.0 - pow(adv.beta2, (double)n)));
+  o.shrink = (float)(1.0 - adv.lr * adv.decay[p]);
+  o.key = mix32(adv.seed_lo + mix32(adv.seed_hi) + (uint32_t)n * 0x632BE5ABu);
+  adv.out[p] = o;
+}
+
+// Closes the pass over the gradients: which tensors are skipped, the norm over
+// the others, the clipping factor and each tensor's t.  One CTA, fixed order:
+// the same gradients give the same bits.
+__device__ void close_pass(const ListTables& t, unsigned pass, double max_norm, const ListAdvance& adv, double* red) {
+  int skipped = 0;
+  for (int p = threadIdx.x; p < t.nparams; p += blockDim.x) {
+    const int sk = __ldcg(&t.mark[p]) == pass;
+    t.skip[p] = sk;
+    skipped += sk;
+    if (adv.step && !sk) adv.step[p] += 1;
+  }
+  __syncthreads();
+  double sum = 0.0;
+  if (__ldcg(&t.result->bad) != pass) {
+    for (int b = threadIdx.x; b < t.nctas; b += blockDim.x) sum += __ldcg(&t.csum[b]);
+  } else {   // without the skipped tensors' chunks
+    for (int i = threadIdx.x; i < t.nchunks * kListWarps; i += blockDim.x)
+      if (!t.skip[t.chunks[i / kListWarps].param]) sum += __ldcg(&t.partial[i]);
+  }
+  sum = block_sum(sum, red);
   const double all = block_sum((double)skipped, red);
   if (threadIdx.x == 0) {
     const double norm = sqrt(sum);
@@ -150,72 +168,122 @@ __device__ void close_pass(const ListTables& t, double max_norm, const ListAdvan
     t.result->coef = max_norm > 0.0 && norm > max_norm ? (float)(max_norm / norm) : 1.0f;
     t.result->skipped = (int)all;
     t.result->done = 0;
+    t.result->pass = pass + 1;
   }
 }
 
-// Sum of squares of one chunk.  Sixteen squares are added in 32 bits, the
-// groups in 64.  A group whose sum is not finite, or so small that its squares
-// may have lost bits below the normal range, is gone through again in 64 bits;
-// that also finds the elements that are not finite.
+// Sums of squares.  Sixteen squares are added in 32 bits, the groups in 64.  A
+// group whose sum is not finite, or so small that its squares may have lost bits
+// below the normal range, is gone through again in 64 bits; that also finds the
+// elements that are not finite.
+//
+// A CTA walks over many chunks with all of a thread's loads of a chunk in
+// flight at once, and its warps join their sums once, at the end.  (A CTA a chunk spent
+// most of its life in the joining: 167 us for 285M bfloat16 elements.)  The sums of each
+// warp's part of a chunk are kept for the case that a tensor has to be left out.
 template <bool BF16, int K>
-__global__ void __launch_bounds__(kThreads) list_norm_kernel(ListTables t, const __grid_constant__ Pointers<K> ptr,
-                                                             int p0, int c0, double max_norm, ListAdvance adv) {
-  __shared__ double red[kThreads / 32];
+__global__ void __launch_bounds__(kThreads, 4) list_norm_kernel(ListTables t, const __grid_constant__ Pointers<K> ptr,
+                                                                int p0, int np, int c0, int nc, int b0, double max_norm,
+                                                                ListAdvance adv) {
+  using V = Vectors<BF16>;
+  __shared__ double red[kListWarps];
   __shared__ bool last;
-  const ListChunk c = t.chunks[c0 + blockIdx.x];
-  const void* g = ptr.p[c.param - p0];
-  const bool al = aligned4<BF16>(g);
-  double sum = 0.0;
-  bool bad = false;
-  for (int i = threadIdx.x * 4; i < c.len; i += 4 * kThreads * 4) {
-    float x[4][4];
+  const unsigned pass = t.result->pass;
+  if (adv.step)
+    for (int p = blockIdx.x * kThreads + threadIdx.x; p < np; p += gridDim.x * kThreads) step_factors(adv, p0 + p);
+  double total = 0.0;
+  for (int i = blockIdx.x; i < nc; i += gridDim.x) {
+    const ListChunk c = t.chunks[c0 + i];
+    const V vec(ptr.p[c.param - p0], c.start, c.len);
+    uint4 u[V::N];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) load4_any<BF16>(g, c.start, i + k * 4 * kThreads, c.len, al, x[k]);
-    float s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) s = fmaf(x[k][q], x[k][q], s);
-    if (s <= FLT_MAX && s >= 0x1p-96f) {
-      sum += (double)s;
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          bad |= !isfinite(x[k][q]);
-          sum += (double)x[k][q] * x[k][q];
-        }
+    for (int k = 0; k < V::N; ++k) {
+      const int v = threadIdx.x + k * kThreads;
+      u[k] = v < vec.nvec ? *vec.at(v) : make_uint4(0, 0, 0, 0);
     }
+    double sum = 0.0;
+    bool bad = false;
+    if (const void* one = vec.single()) {
+      const float x = load1<BF16>(one, 0);
+      bad = !isfinite(x);
+      sum = (double)x * x;
+    }
+    constexpr int G = 16 / V::E;   // vectors of sixteen elements
+#pragma unroll
+    for (int k = 0; k < V::N; k += G) {
+      float x[16];
+#pragma unroll
+      for (int j = 0; j < G; ++j) widen<BF16>(u[k + j], x + j * V::E);
+      float s = 0.0f;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) s = fmaf(x[q], x[q], s);
+      if (s <= FLT_MAX && s >= 0x1p-96f) {
+        sum += (double)s;
+      } else {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          bad |= !isfinite(x[q]);
+          sum += (double)x[q] * x[q];
+        }
+      }
+    }
+    sum = warp_sum(sum);
+    if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) t.mark[c.param] = t.result->bad = pass;
+    if ((threadIdx.x & 31) == 0) t.partial[(int64_t)(c0 + i) * kListWarps + (threadIdx.x >> 5)] = sum;
+    total += sum;
   }
-  sum = block_sum(sum, red);
-  const bool any = __syncthreads_or(bad);
+  // every lane of a warp holds its warp's total
+  const double sum = block_sum((threadIdx.x & 31) == 0 ? total : 0.0, red);
+  __threadfence();
+  __syncthreads();
   if (threadIdx.x == 0) {
-    t.partial[c0 + blockIdx.x] = any ? nan("") : sum;
+    t.csum[b0 + blockIdx.x] = sum;
     __threadfence();
-    last = atomicAdd(&t.result->done, 1u) == (unsigned)t.nchunks - 1;
+    last = atomicAdd(&t.result->done, 1u) == (unsigned)t.nctas - 1;
   }
   __syncthreads();
   if (!last) return;
   __threadfence();
-  close_pass(t, max_norm, adv, red);
+  close_pass(t, pass, max_norm, adv, red);
 }
 
+// The chunks in the reverse of the norm's order: what it read last is still in L2.
 template <bool BF16, int K>
 __global__ void __launch_bounds__(kThreads) list_scale_kernel(ListTables t, const __grid_constant__ Pointers<K> ptr,
                                                               int p0, int c0) {
+  using V = Vectors<BF16>;
   const float coef = t.result->coef;
   if (coef == 1.0f) return;
-  const ListChunk c = t.chunks[c0 + blockIdx.x];
+  const ListChunk c = t.chunks[c0 + gridDim.x - 1 - blockIdx.x];
   if (t.skip[c.param]) return;
-  void* g = const_cast<void*>(ptr.p[c.param - p0]);
-  const bool al = aligned4<BF16>(g);
-  for (int i = threadIdx.x * 4; i < c.len; i += 4 * kThreads) {
-    float x[4];
-    load4_any<BF16>(g, c.start, i, c.len, al, x);
+  const V vec(ptr.p[c.param - p0], c.start, c.len);
+  uint4 u[V::N];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) x[q] *= coef;
-    store4_any<BF16>(g, c.start, i, c.len, al, x);
+  for (int k = 0; k < V::N; ++k) {
+    const int v = threadIdx.x + k * kThreads;
+    if (v < vec.nvec) u[k] = *vec.at(v);
+  }
+  if (void* one = vec.single()) store1<BF16>(one, 0, load1<BF16>(one, 0) * coef);
+#pragma unroll
+  for (int k = 0; k < V::N; ++k) {
+    const int v = threadIdx.x + k * kThreads;
+    if (v >= vec.nvec) continue;
+    float x[V::E];
+    widen<BF16>(u[k], x);
+#pragma unroll
+    for (int q = 0; q < V::E; ++q) x[q] *= coef;
+    uint4 o;
+    if (BF16) {
+      uint32_t* w = &o.x;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * q], x[2 * q + 1]);
+        w[q] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    } else {
+      o = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+    *vec.at(v) = o;
   }
 }
 
@@ -225,48 +293,102 @@ struct Hyper {
   float beta1, omb1, beta2, omb2, eps;
 };
 
-// One element; m and v come back updated.  Both stop at the largest float instead of
-// becoming an infinity that they would never leave.  Products and sums of the moments are
-// rounded one by one, as written: left to the compiler to fuse, a last bit that came out
-// differently in another build would round to another 8-bit code.
-__device__ __forceinline__ float adamw1(float w, float g, float& m, float& v, float& r, const ListStep& s,
-                                        const Hyper& h) {
-  m = __fadd_rn(__fmul_rn(h.beta1, m), __fmul_rn(h.omb1, g));
-  m = fminf(fmaxf(m, -FLT_MAX), FLT_MAX);
-  v = __fadd_rn(__fmul_rn(h.beta2, v), __fmul_rn(__fmul_rn(h.omb2, g), g));
-  v = fminf(v, FLT_MAX);
-  r = sqrtf(v);
-  return fmaf(w, s.shrink, -s.first * (m / fmaf(r, s.second, h.eps)));
+// What a CTA of the update needs to know of its chunk.
+struct Update {
+  ListChunk c;
+  ListStep s;
+  float coef;
+  bool huge;       // a gradient element may have a square beyond the largest float
+  float* w;
+  const void* g;
+  uint16_t* b;     // the bfloat16 copy, or null
+};
+
+// The chunks in the reverse of the norm's order: the gradients that it read last
+// are still in L2.  False where the tensor is skipped.
+template <int K>
+__device__ __forceinline__ bool update_of(Update& u, const ListTables& t, const Pointers<K>& wp, const Pointers<K>& gp,
+                                          const Pointers<K>& cp, int copies, int p0, int c0, const ListStep* step) {
+  u.c = t.chunks[c0 + gridDim.x - 1 - blockIdx.x];
+  if (t.skip[u.c.param]) return false;
+  u.s = step[u.c.param];
+  u.coef = t.result->coef;
+  u.huge = !(t.result->norm * u.coef < kGradMax);   // no element exceeds the norm
+  u.w = static_cast<float*>(const_cast<void*>(wp.p[u.c.param - p0])) + u.c.start;
+  u.g = gp.p[u.c.param - p0];
+  u.b = copies ? static_cast<uint16_t*>(const_cast<void*>(cp.p[u.c.param - p0])) + u.c.start : nullptr;
+  return true;
 }
 
+__device__ __forceinline__ float limit(float g) { return fminf(fmaxf(g, -kGradMax), kGradMax); }
+
+// Products and sums of the moments are rounded one by one, as written: left to the
+// compiler to fuse, a last bit that came out differently in another build would round
+// to another 8-bit code.
+__device__ __forceinline__ float next_m(float b1m, float g, const Hyper& h) {
+  return __fadd_rn(b1m, __fmul_rn(h.omb1, g));
+}
+__device__ __forceinline__ float next_v(float b2v, float g, const Hyper& h) {
+  return __fadd_rn(b2v, __fmul_rn(__fmul_rn(h.omb2, g), g));
+}
+// The quotient by the fast reciprocal: 2 units in the last place of a term that moves
+// the weight by about lr.
+__device__ __forceinline__ float next_w(float w, float m, float r, const ListStep& s, const Hyper& h) {
+  return fmaf(w, s.shrink, -s.first * __fdividef(m, fmaf(r, s.second, h.eps)));
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ uint2 bf16_bits4(const float* x) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// One thread steps four elements at a time where the tensor's pointers are aligned to
+// four, and single ones, neighbouring threads neighbouring elements, where not.
 template <bool BF16, int K>
 __global__ void __launch_bounds__(kThreads) adamw_f32_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
                                                              const __grid_constant__ Pointers<K> gp,
                                                              const __grid_constant__ Pointers<K> cp, int copies,
                                                              int p0, int c0, AdamwState st,
                                                              const ListStep* __restrict__ step, Hyper h) {
-  const ListChunk c = t.chunks[c0 + blockIdx.x];
-  if (t.skip[c.param]) return;
-  const ListStep s = step[c.param];
-  const float coef = t.result->coef;
-  float* w = static_cast<float*>(const_cast<void*>(wp.p[c.param - p0]));
-  const void* g = gp.p[c.param - p0];
-  void* b = copies ? const_cast<void*>(cp.p[c.param - p0]) : nullptr;
-  const bool alw = aligned4<false>(w), alg = aligned4<BF16>(g), alb = aligned4<true>(b);
-  float *m = st.m + c.flat, *v = st.v + c.flat;
-  // the flat state is padded to whole blocks: its loads and stores may pass len
-  for (int i = threadIdx.x * 4; i < c.len; i += 4 * kThreads) {
-    float xw[4], xg[4], xm[4], xv[4], r;
-    load4_any<false>(w, c.start, i, c.len, alw, xw);
-    load4_any<BF16>(g, c.start, i, c.len, alg, xg);
-    load4<false>(m, i, xm);
-    load4<false>(v, i, xv);
+  Update u;
+  if (!update_of(u, t, wp, gp, cp, copies, p0, c0, step)) return;
+  float *m = st.m + u.c.flat, *v = st.v + u.c.flat;
+  int done = 0;
+  if (aligned4<false>(u.w) && aligned4<BF16>(u.g) && aligned4<true>(u.b)) {
+    done = u.c.len & ~3;
+#pragma unroll 2
+    for (int i = threadIdx.x * 4; i < done; i += 4 * kThreads) {
+      float xw[4], xg[4], xm[4], xv[4];
+      load4<false>(u.w, i, xw);
+      load4<BF16>(u.g, u.c.start + i, xg);
+      load4<false>(m, i, xm);
+      load4<false>(v, i, xv);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) xw[q] = adamw1(xw[q], __fmul_rn(xg[q], coef), xm[q], xv[q], r, s, h);
-    store4_any<false>(w, c.start, i, c.len, alw, xw);
-    if (b) store4_any<true>(b, c.start, i, c.len, alb, xw);
-    store4<false>(m, i, xm);
-    store4<false>(v, i, xv);
+      for (int q = 0; q < 4; ++q) {
+        float g = __fmul_rn(xg[q], u.coef);
+        if (u.huge) g = limit(g);
+        xm[q] = next_m(__fmul_rn(h.beta1, xm[q]), g, h);
+        xv[q] = next_v(__fmul_rn(h.beta2, xv[q]), g, h);
+        xw[q] = next_w(xw[q], xm[q], sqrtf(xv[q]), u.s, h);
+      }
+      store4<false>(u.w, i, xw);
+      store4<false>(m, i, xm);
+      store4<false>(v, i, xv);
+      if (u.b) *reinterpret_cast<uint2*>(u.b + i) = bf16_bits4(xw);
+    }
+  }
+#pragma unroll 4
+  for (int i = done + threadIdx.x; i < u.c.len; i += kThreads) {
+    float g = __fmul_rn(load1<BF16>(u.g, u.c.start + i), u.coef);
+    if (u.huge) g = limit(g);
+    const float xm = next_m(__fmul_rn(h.beta1, m[i]), g, h);
+    const float xv = next_v(__fmul_rn(h.beta2, v[i]), g, h);
+    const float xw = next_w(u.w[i], xm, sqrtf(xv), u.s, h);
+    u.w[i] = xw;
+    m[i] = xm;
+    v[i] = xv;
+    if (u.b) u.b[i] = bf16_bits(xw);
   }
 }
 
@@ -293,106 +415,219 @@ __device__ __forceinline__ int scale_byte(uint32_t largest_bits) {
 }
 // 2^(E - 127), zero for the byte 0 of a fresh state
 __device__ __forceinline__ float scale_of(int e) { return __uint_as_float((uint32_t)e << 23); }
-// its reciprocal 2^(127 - E); E is at most 247, the byte of the largest float
+// its reciprocal 2^(127 - E)
 __device__ __forceinline__ float inverse_scale(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
+
+// Two floats that the packed instructions of sm_100 work on, each rounded as alone.
+struct F2 {
+  unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float a, float b) {
+  F2 o;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(o.v) : "f"(a), "f"(b));
+  return o;
+}
+__device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ float2 un2(F2 a) {
+  float2 o;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(a.v));
+  return o;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+  F2 o;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(o.v) : "l"(a.v), "l"(b.v));
+  return o;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+  F2 o;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(o.v) : "l"(a.v), "l"(b.v));
+  return o;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 o;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(o.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return o;
+}
+__device__ __forceinline__ F2 minus(F2 a, F2 b) { return fma2(b, f2(-1.0f), a); }   // exact as a - b
+
+__device__ __forceinline__ float lift_of(float a) { return a < 0x1p-6f ? 0x1p-6f : 0.0f; }
+__device__ __forceinline__ F2 masked(F2 a, uint32_t mask) {
+  const float2 x = un2(a);
+  return f2(__uint_as_float(__float_as_uint(x.x) & mask), __uint_as_float(__float_as_uint(x.y) & mask));
+}
 
 // a in [0, 448] to a value of e4m3, up where the 16 random bits and the 20 bits
 // that are cut off carry.  Below 2^-6 the codes are 2^-9 apart throughout, as they
 // are in [2^-6, 2^-5): values there are lifted by 2^-6 for the rounding.
-__device__ __forceinline__ float round_m(float a, uint32_t bits16) {
-  const float lift = a < 0x1p-6f ? 0x1p-6f : 0.0f;
-  return __uint_as_float((__float_as_uint(a + lift) + (bits16 << 4)) & 0xFFF00000u) - lift;
+__device__ __forceinline__ F2 round_m(float a0, float a1, uint32_t bits0, uint32_t bits1) {
+  const F2 lift = f2(lift_of(a0), lift_of(a1));
+  const float2 x = un2(f2(a0, a1) + lift);
+  const F2 y = f2(__uint_as_float((__float_as_uint(x.x) + (bits0 << 4)) & 0xFFF00000u),
+                  __uint_as_float((__float_as_uint(x.y) + (bits1 << 4)) & 0xFFF00000u));
+  return minus(y, lift);
 }
-__device__ __forceinline__ float round_r(float a, uint32_t bits16) {
-  const float lift = a < 0x1p-6f ? 0x1p-6f : 0.0f;
-  const uint32_t word = __float_as_uint(a + lift);
-  const float lo = __uint_as_float(word & 0xFFF00000u) - lift;
-  const float gap = __uint_as_float(word & 0x7F800000u) * 0.125f;
-  const bool up = (a - lo) * (a + lo) > (float)bits16 * 0x1p-16f * (gap * fmaf(2.0f, lo, gap));
-  return up ? lo + gap : lo;
+__device__ __forceinline__ F2 round_r(F2 a, uint32_t bits0, uint32_t bits1) {
+  const float2 s = un2(a);
+  const F2 lift = f2(lift_of(s.x), lift_of(s.y));
+  const F2 word = a + lift;
+  const F2 lo = minus(masked(word, 0xFFF00000u), lift);
+  const F2 gap = masked(word, 0x7F800000u) * f2(0.125f);
+  const F2 hi = lo + gap;
+  // bits / 2^16, from the significand of a number in [1, 2)
+  const F2 chance = f2(__uint_as_float(bits0 * 128 + 0x3F800000u), __uint_as_float(bits1 * 128 + 0x3F800000u)) + f2(-1.0f);
+  const float2 p = un2(minus(a, lo) * (a + lo)), q = un2(chance * (gap * (lo + hi)));
+  const float2 l = un2(lo), u = un2(hi);
+  return f2(p.x > q.x ? u.x : l.x, p.y > q.y ? u.y : l.y);
 }
 
-__device__ __forceinline__ void unpack4(uint32_t codes, float (&x)[4]) {
+// Codes to floats and back; values of e4m3 convert exactly.
+__device__ __forceinline__ float2 code_values(uint32_t two) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
+}
+__device__ __forceinline__ uint32_t value_codes(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+
+// One warp steps one block: eight elements a lane.  Whole: the block is full and
+// the pointers are aligned to four elements; lane l holds elements 4l..4l+3 of
+// either half.  Otherwise element 32 q + l is lane l's q-th, so that accesses of single elements
+// are those of neighbouring lanes to neighbouring addresses.
+template <bool BF16, bool WHOLE>
+__device__ __forceinline__ void step_block(const Update& u, int o, const AdamwState& st, const Hyper& h) {
+  const int lane = threadIdx.x & 31;
+  const int64_t flat = u.c.flat + o, blk = flat / kQBlock;
+  const auto at = [&](int q) { return WHOLE ? 128 * (q >> 2) + 4 * lane + (q & 3) : 32 * q + lane; };
+  const auto in = [&](int q) { return WHOLE || o + at(q) < u.c.len; };
+  uint8_t *mq = st.mq + flat, *rq = st.rq + flat;
+  float* w = u.w + o;
+  float xw[8], xg[8], m[8], r[8];
+  const int em0 = st.ms[blk], er0 = st.rs[blk];
+  if (WHOLE) {
+    uint32_t cm[2], cr[2];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(codes >> (16 * k)), __NV_E4M3));
-    const float2 f = __half22float2(h);
-    x[2 * k] = f.x;
-    x[2 * k + 1] = f.y;
+    for (int k = 0; k < 2; ++k) {
+      const int i = 128 * k + 4 * lane;
+      load4<false>(w, i, *reinterpret_cast<float(*)[4]>(xw + 4 * k));
+      load4<BF16>(u.g, u.c.start + o + i, *reinterpret_cast<float(*)[4]>(xg + 4 * k));
+      cm[k] = *reinterpret_cast<const uint32_t*>(mq + i);
+      cr[k] = *reinterpret_cast<const uint32_t*>(rq + i);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 a = code_values(cm[k >> 1] >> (16 * (k & 1))), b = code_values(cr[k >> 1] >> (16 * (k & 1)));
+      m[2 * k] = a.x;
+      m[2 * k + 1] = a.y;
+      r[2 * k] = b.x;
+      r[2 * k + 1] = b.y;
+    }
+  } else {
+    uint8_t cm[8], cr[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      xw[q] = in(q) ? w[at(q)] : 0.0f;
+      xg[q] = in(q) ? load1<BF16>(u.g, u.c.start + o + at(q)) : 0.0f;
+      cm[q] = mq[at(q)];
+      cr[q] = rq[at(q)];
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      m[q] = code_values(cm[q]).x;
+      r[q] = code_values(cr[q]).x;
+    }
+  }
+  const float ms = scale_of(em0), rs = scale_of(er0);
+  // b1 (code * scale) is (b1 scale) code: the scale is a power of two
+  const F2 b1ms = f2(h.beta1 * ms), rs2 = f2(rs);
+  float mm = 0.0f, rm = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    F2 g = f2(xg[k], xg[k + 1]) * f2(u.coef);
+    if (u.huge) {
+      const float2 x = un2(g);
+      g = f2(limit(x.x), limit(x.y));
+    }
+    const float2 xm = un2(f2(m[k], m[k + 1]) * b1ms + f2(h.omb1) * g);
+    const F2 r0 = f2(r[k], r[k + 1]) * rs2;
+    const float2 v = un2(f2(h.beta2) * (r0 * r0) + f2(h.omb2) * g * g);
+    m[k] = xm.x;
+    m[k + 1] = xm.y;
+    r[k] = sqrtf(v.x);
+    r[k + 1] = sqrtf(v.y);
+    const float2 d = un2(fma2(f2(r[k], r[k + 1]), f2(u.s.second), f2(h.eps)));
+    const F2 move = f2(-u.s.first) * f2(__fdividef(xm.x, d.x), __fdividef(xm.y, d.y));
+    const float2 x = un2(fma2(f2(xw[k], xw[k + 1]), f2(u.s.shrink), move));
+    xw[k] = x.x;
+    xw[k + 1] = x.y;
+    mm = fmaxf(mm, fmaxf(fabsf(xm.x), fabsf(xm.y)));
+    rm = fmaxf(rm, fmaxf(r[k], r[k + 1]));
+  }
+  if (WHOLE) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = 128 * k + 4 * lane;
+      store4<false>(w, i, *reinterpret_cast<const float(*)[4]>(xw + 4 * k));
+      if (u.b) *reinterpret_cast<uint2*>(u.b + o + i) = bf16_bits4(xw + 4 * k);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (!in(q)) continue;
+      w[at(q)] = xw[q];
+      if (u.b) u.b[o + at(q)] = bf16_bits(xw[q]);
+    }
+  }
+  // magnitudes order as their bits do
+  const int em = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(mm)));
+  const int er = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(rm)));
+  const float im = inverse_scale(em);
+  const F2 ir = f2(inverse_scale(er));
+  const uint32_t base = (uint32_t)flat * 0x9E3779B1u + (uint32_t)(flat >> 32) * 0x85EBCA77u + u.s.key;
+  const uint32_t lane_base = base + (uint32_t)at(0) * 0x9E3779B1u;
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    const uint32_t h0 = mix32(lane_base + (uint32_t)(at(k) - at(0)) * 0x9E3779B1u);
+    const uint32_t h1 = mix32(lane_base + (uint32_t)(at(k + 1) - at(0)) * 0x9E3779B1u);
+    const float2 x = un2(round_m(fabsf(m[k] * im), fabsf(m[k + 1] * im), h0 & 0xFFFFu, h1 & 0xFFFFu));
+    m[k] = copysignf(x.x, m[k]);
+    m[k + 1] = copysignf(x.y, m[k + 1]);
+    const float2 y = un2(round_r(f2(r[k], r[k + 1]) * ir, h0 >> 16, h1 >> 16));
+    r[k] = y.x;
+    r[k + 1] = y.y;
+  }
+  if (WHOLE) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int i = 128 * k + 4 * lane;
+      *reinterpret_cast<uint32_t*>(mq + i) =
+          value_codes(m[4 * k], m[4 * k + 1]) | (value_codes(m[4 * k + 2], m[4 * k + 3]) << 16);
+      *reinterpret_cast<uint32_t*>(rq + i) =
+          value_codes(r[4 * k], r[4 * k + 1]) | (value_codes(r[4 * k + 2], r[4 * k + 3]) << 16);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {   // behind the tensor's end: zeros, as they were
+      mq[at(q)] = (uint8_t)value_codes(m[q], 0.0f);
+      rq[at(q)] = (uint8_t)value_codes(r[q], 0.0f);
+    }
+  }
+  if (lane == 0) {
+    st.ms[blk] = (uint8_t)em;
+    st.rs[blk] = (uint8_t)er;
   }
 }
-// values of e4m3 already: the conversion is exact
-__device__ __forceinline__ uint32_t pack4(const float (&x)[4]) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
-  return lo | (hi << 16);
-}
 
-// One warp per block of 256: lane l holds elements 4l..4l+3 of either half.
 template <bool BF16, int K>
-__global__ void __launch_bounds__(kThreads) adamw_8bit_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
-                                                              const __grid_constant__ Pointers<K> gp,
-                                                              const __grid_constant__ Pointers<K> cp, int copies,
-                                                              int p0, int c0, AdamwState st,
-                                                              const ListStep* __restrict__ step, Hyper h) {
-  const ListChunk c = t.chunks[c0 + blockIdx.x];
-  if (t.skip[c.param]) return;
-  const ListStep s = step[c.param];
-  const float coef = t.result->coef;
-  float* w = static_cast<float*>(const_cast<void*>(wp.p[c.param - p0]));
-  const void* g = gp.p[c.param - p0];
-  void* b = copies ? const_cast<void*>(cp.p[c.param - p0]) : nullptr;
-  const bool alw = aligned4<false>(w), alg = aligned4<BF16>(g), alb = aligned4<true>(b);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int o = warp * kQBlock; o < c.len; o += (kThreads / 32) * kQBlock) {
-    const int64_t flat = c.flat + o, blk = flat / kQBlock;
-    const float ms = scale_of(st.ms[blk]), rs = scale_of(st.rs[blk]);
-    float xw[2][4], xg[2][4], xm[2][4], xr[2][4];
-    float mm = 0.0f, rm = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int i = o + 128 * k + 4 * lane;
-      load4_any<false>(w, c.start, i, c.len, alw, xw[k]);
-      load4_any<BF16>(g, c.start, i, c.len, alg, xg[k]);
-      unpack4(*reinterpret_cast<const uint32_t*>(st.mq + c.flat + i), xm[k]);
-      unpack4(*reinterpret_cast<const uint32_t*>(st.rq + c.flat + i), xr[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float m = xm[k][q] * ms, r = xr[k][q] * rs, v = __fmul_rn(r, r);
-        xw[k][q] = adamw1(xw[k][q], __fmul_rn(xg[k][q], coef), m, v, r, s, h);
-        xm[k][q] = m;
-        xr[k][q] = r;
-        mm = fmaxf(mm, fabsf(m));
-        rm = fmaxf(rm, r);
-      }
-      const int i = o + 128 * k + 4 * lane;
-      store4_any<false>(w, c.start, i, c.len, alw, xw[k]);
-      if (b) store4_any<true>(b, c.start, i, c.len, alb, xw[k]);
-    }
-    // magnitudes order as their bits do
-    const int em = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(mm)));
-    const int er = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(rm)));
-    const float im = inverse_scale(em), ir = inverse_scale(er);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int64_t j = flat + 128 * k + 4 * lane;
-      const uint32_t base = (uint32_t)j * 0x9E3779B1u + (uint32_t)(j >> 32) * 0x85EBCA77u + s.key;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t bits = mix32(base + q * 0x9E3779B1u);
-        xm[k][q] = copysignf(round_m(fabsf(xm[k][q]) * im, bits & 0xFFFFu), xm[k][q]);
-        xr[k][q] = round_r(xr[k][q] * ir, bits >> 16);
-      }
-      *reinterpret_cast<uint32_t*>(st.mq + j) = pack4(xm[k]);
-      *reinterpret_cast<uint32_t*>(st.rq + j) = pack4(xr[k]);
-    }
-    if (lane == 0) {
-      st.ms[blk] = (uint8_t)em;
-      st.rs[blk] = (uint8_t)er;
-    }
+__global__ void __launch_bounds__(kThreads, 3) adamw_8bit_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
+                                                                 const __grid_constant__ Pointers<K> gp,
+                                                                 const __grid_constant__ Pointers<K> cp, int copies,
+                                                                 int p0, int c0, AdamwState st,
+                                                                 const ListStep* __restrict__ step, Hyper h) {
+  Update u;
+  if (!update_of(u, t, wp, gp, cp, copies, p0, c0, step)) return;
+  const bool aligned = aligned4<false>(u.w) && aligned4<BF16>(u.g) && aligned4<true>(u.b);
+  for (int o = (threadIdx.x >> 5) * kQBlock; o < u.c.len; o += kListWarps * kQBlock) {
+    if (aligned && o + kQBlock <= u.c.len) step_block<BF16, true>(u, o, st, h);
+    else step_block<BF16, false>(u, o, st, h);
   }
 }
 
@@ -415,13 +650,20 @@ cudaError_t by_count(int n, F&& f) {
 
 }  // namespace
 
-cudaError_t launch_list_norm(const ListTables& t, const void* const* g, int p0, int np, int c0, int nc, int bf16,
+// Four CTAs an SM; fewer where that lets all of them walk over equally many chunks.
+int list_norm_ctas(int nc) {
+  const int rounds = (nc + 4 * kSms - 1) / (4 * kSms);
+  return (nc + rounds - 1) / rounds;
+}
+
+cudaError_t launch_list_norm(const ListTables& t, const void* const* g, int p0, int np, int c0, int nc, int b0, int bf16,
                              double max_norm, const ListAdvance& adv, cudaStream_t s) {
   return by_count(np, [&](auto n) {
     constexpr int K = decltype(n)::value;
     const Pointers<K> a = pack<K>(g + p0, np);
-    if (bf16) list_norm_kernel<true, K><<<nc, kThreads, 0, s>>>(t, a, p0, c0, max_norm, adv);
-    else list_norm_kernel<false, K><<<nc, kThreads, 0, s>>>(t, a, p0, c0, max_norm, adv);
+    const int ctas = list_norm_ctas(nc);
+    if (bf16) list_norm_kernel<true, K><<<ctas, kThreads, 0, s>>>(t, a, p0, np, c0, nc, b0, max_norm, adv);
+    else list_norm_kernel<false, K><<<ctas, kThreads, 0, s>>>(t, a, p0, np, c0, nc, b0, max_norm, adv);
   });
 }
 

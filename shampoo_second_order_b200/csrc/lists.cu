@@ -4,6 +4,7 @@
 // pointers on the host and launches its kernels, nothing else: no copy, no
 // allocation and no wait, so a call can be captured into a graph.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <memory>
 #include <new>
@@ -25,6 +26,7 @@ namespace {
 // A run of at most kListGroup tensors and of their chunks: one launch of each kernel.
 struct Group {
   int p0, np, c0, nc;
+  int b0;   // first of its CTAs in the pass over the gradients
 };
 
 // The list itself, common to both contexts.
@@ -105,7 +107,7 @@ shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dt
   l->numel.assign(numel, numel + nparams);
   std::vector<ListChunk> chunks;
   for (int i = 0; i < nparams; ++i) {
-    if (i % kListGroup == 0) l->groups.push_back(Group{i, 0, (int)chunks.size(), 0});
+    if (i % kListGroup == 0) l->groups.push_back(Group{i, 0, (int)chunks.size(), 0, 0});
     l->offset.push_back(l->total);
     for (int64_t s = 0; s < numel[i]; s += kListChunk) {
       ListChunk c{};
@@ -123,12 +125,20 @@ shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dt
   l->tab.nchunks = (int)chunks.size();
   l->tab.nparams = nparams;
   ListChunk* d = nullptr;
-  if ((e = zeroed(l, &d, l->tab.nchunks)) != cudaSuccess || (e = zeroed(l, &l->tab.partial, l->tab.nchunks)) != cudaSuccess ||
-      (e = zeroed(l, &l->tab.skip, nparams)) != cudaSuccess || (e = zeroed(l, &l->tab.result, 1)) != cudaSuccess)
+  for (Group& g : l->groups) {
+    g.b0 = l->tab.nctas;
+    l->tab.nctas += list_norm_ctas(g.nc);
+  }
+  if ((e = zeroed(l, &d, l->tab.nchunks)) != cudaSuccess || (e = zeroed(l, &l->tab.partial, (int64_t)l->tab.nchunks * kListWarps)) != cudaSuccess ||
+      (e = zeroed(l, &l->tab.csum, l->tab.nctas)) != cudaSuccess ||
+      (e = zeroed(l, &l->tab.mark, nparams)) != cudaSuccess || (e = zeroed(l, &l->tab.skip, nparams)) != cudaSuccess || (e = zeroed(l, &l->tab.result, 1)) != cudaSuccess)
     return refuse(l, SHAMPOO_ENOMEM, std::string("device allocation failed: ") + cudaGetErrorString(e));
   l->tab.chunks = d;
-  // pageable source: staged by the driver before the call returns
-  e = cudaMemcpyAsync(d, chunks.data(), chunks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
+  // pageable sources: staged by the driver before the calls return
+  const ListResult first{0.f, 1.f, 0, 0, 1, 0};
+  e = cudaMemcpyAsync(l->tab.result, &first, sizeof(first), cudaMemcpyHostToDevice, l->stream);
+  if (e == cudaSuccess)
+    e = cudaMemcpyAsync(d, chunks.data(), chunks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
   if (e != cudaSuccess) return cuda_error(l, e, "upload of the chunk table");
   return SHAMPOO_OK;
 }
@@ -256,7 +266,7 @@ shampoo_status shampoo_clip_norm(shampoo_clip* clip, const void* const* grads) {
     if (st != SHAMPOO_OK) return st;
     OnDevice on(l->device);
     for (const Group& g : l->groups) {
-      const cudaError_t e = launch_list_norm(l->tab, grads, g.p0, g.np, g.c0, g.nc, l->bf16, 0.0, ListAdvance{}, l->stream);
+      const cudaError_t e = launch_list_norm(l->tab, grads, g.p0, g.np, g.c0, g.nc, g.b0, l->bf16, 0.0, ListAdvance{}, l->stream);
       if (e != cudaSuccess) return cuda_error(l, e, "list_norm");
     }
     return SHAMPOO_OK;
@@ -276,7 +286,7 @@ shampoo_status shampoo_clip_apply(shampoo_clip* clip, void* const* grads, double
     OnDevice on(l->device);
     cudaError_t e = cudaSuccess;
     for (const Group& g : l->groups)
-      if ((e = launch_list_norm(l->tab, g0, g.p0, g.np, g.c0, g.nc, l->bf16, max_norm, ListAdvance{}, l->stream)) != cudaSuccess)
+      if ((e = launch_list_norm(l->tab, g0, g.p0, g.np, g.c0, g.nc, g.b0, l->bf16, max_norm, ListAdvance{}, l->stream)) != cudaSuccess)
         return cuda_error(l, e, "list_norm");
     for (const Group& g : l->groups)
       if ((e = launch_list_scale(l->tab, grads, g.p0, g.np, g.c0, g.nc, l->bf16, l->stream)) != cudaSuccess)
@@ -325,8 +335,9 @@ shampoo_status shampoo_adamw_create(shampoo_adamw** out, int nparams, const int6
     if (st != SHAMPOO_OK) return st;
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0))
       return refuse(nullptr, SHAMPOO_EINVAL, "beta1 and beta2 must be in [0, 1)");
-    // held in 32 bits on the device: a denominator of zero would follow from one that rounds to it
-    if (!((float)epsilon > 0.f) || !std::isfinite((float)epsilon)) return refuse(nullptr, SHAMPOO_EINVAL, "epsilon must be > 0");
+    // held in 32 bits on the device, which divides by it where v is zero: a subnormal would count as zero there
+    if (!((float)epsilon >= FLT_MIN) || !std::isfinite((float)epsilon))
+      return refuse(nullptr, SHAMPOO_EINVAL, "epsilon must be finite and at least 1.18e-38");
     if (state_bits != 32 && state_bits != 8) return refuse(nullptr, SHAMPOO_EINVAL, "state_bits must be 32 or 8");
     if (!(max_norm >= 0.0) || !std::isfinite(max_norm)) return refuse(nullptr, SHAMPOO_EINVAL, "max_norm must be >= 0 (0: no clipping)");
     for (int i = 0; weight_decay && i < nparams; ++i)
@@ -389,7 +400,7 @@ shampoo_status shampoo_adamw_step(shampoo_adamw* adamw, float* const* params, co
     const ListAdvance adv{a->step, a->factors, a->decay, lr, a->beta1, a->beta2, (uint32_t)a->seed, (uint32_t)(a->seed >> 32)};
     cudaError_t e = cudaSuccess;
     for (const Group& g : l->groups)
-      if ((e = launch_list_norm(l->tab, grads, g.p0, g.np, g.c0, g.nc, l->bf16, a->max_norm, adv, l->stream)) != cudaSuccess)
+      if ((e = launch_list_norm(l->tab, grads, g.p0, g.np, g.c0, g.nc, g.b0, l->bf16, a->max_norm, adv, l->stream)) != cudaSuccess)
         return cuda_error(l, e, "list_norm");
     for (const Group& g : l->groups)
       if ((e = launch_adamw(l->tab, params, grads, copies, g.p0, g.np, g.c0, g.nc, l->bf16, a->bits == 8, a->st, a->factors,

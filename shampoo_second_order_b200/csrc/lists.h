@@ -7,6 +7,7 @@
 namespace shampoo {
 
 constexpr int kListChunk = 8192;   // elements per CTA of the list kernels
+constexpr int kListWarps = 8;      // warps per CTA of the list kernels
 constexpr int kQBlock = 256;       // elements per scale of the 8-bit moments; every
                                    // tensor's state starts at a multiple of it
 
@@ -24,6 +25,8 @@ struct ListResult {
   float coef;       // the clipping factor, 1 without clipping
   int skipped;      // tensors whose gradient is not finite
   unsigned done;    // CTAs of the pass that have finished (zero between passes)
+  unsigned pass;    // number of this pass, from 1 on
+  unsigned bad;     // the last pass that met an element that is not finite
 };
 
 // Per-tensor factors of one AdamW step.
@@ -34,7 +37,7 @@ struct ListStep {
   uint32_t key;     // of the stochastic rounding's hash
 };
 
-// AdamW's part of the pass's end: advance t and set ListStep (null step: none).
+// AdamW's part of the pass: advance t and set ListStep (null step: none).
 struct ListAdvance {
   int* step;              // [n] t of each tensor
   ListStep* out;          // [n]
@@ -46,10 +49,13 @@ struct ListAdvance {
 // The tables of a pass over the gradients.
 struct ListTables {
   const ListChunk* chunks;
-  double* partial;        // [nchunks] sum of squares, NaN where an element is not finite
-  int* skip;              // [n] 1: the tensor's gradient is not finite
+  double* partial;        // [nchunks][kListWarps] sum of squares of each warp's part of a chunk
+  double* csum;           // [nctas] and of all that a CTA of the pass has read
+  unsigned* mark;         // [n] the last pass that met an element of it that is not finite
+  int* skip;              // [n] 1: the tensor's gradient was not finite
   ListResult* result;
   int nchunks, nparams;
+  int nctas;              // of the pass, over all its launches
 };
 
 // Tensor pointers travel as kernel arguments, so that a captured launch keeps
@@ -61,9 +67,11 @@ struct AdamwState {
   uint8_t *mq, *rq, *ms, *rs;   // 8-bit: codes of m and sqrt(v), scale exponents
 };
 
-// The norm of the tensors [p0, p0 + np), whose chunks are [c0, c0 + nc); the launch
-// that finishes last closes the pass over all chunks.
-cudaError_t launch_list_norm(const ListTables& t, const void* const* g, int p0, int np, int c0, int nc, int bf16,
+// CTAs of the norm's launch over nc chunks.
+int list_norm_ctas(int nc);
+// The norm of the tensors [p0, p0 + np), whose chunks are [c0, c0 + nc), by CTAs that are the
+// pass's b0th and following; the CTA that finishes last closes the pass over all chunks.
+cudaError_t launch_list_norm(const ListTables& t, const void* const* g, int p0, int np, int c0, int nc, int b0, int bf16,
                              double max_norm, const ListAdvance& adv, cudaStream_t s);
 cudaError_t launch_list_scale(const ListTables& t, void* const* g, int p0, int np, int c0, int nc, int bf16,
                               cudaStream_t s);

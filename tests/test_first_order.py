@@ -11,8 +11,8 @@ bfloat16.  All tests compare elementwise with a count of roundings:
   v       1 - b2 or b2 (1), two products or one (2), with 8 bits the square v starts from (1), the sum (1),
           g twice (20): all terms positive, 6 u v' and 20 u with clipping
   r       half of v's and the root's own: 4 u, and 10 u with clipping
-  step    lr/(1-b1^t) (1), 1/sqrt(1-b2^t) (1), eps (1), the fma (1), the division (1), the product (1):
-          7 u of it with r's part, and m's error times its factor
+  step    lr/(1-b1^t) (1), 1/sqrt(1-b2^t) (1), eps (1), the fma (1), the fast division (2 units in the last
+          place: 4), the product (1): 9 u of it, r's part, and m's error times its factor
   w       shrink (1) and the last fma (1): u (|w| + |w'|) on top
 Second-order terms are covered by a last factor of 1.01.
 """
@@ -27,6 +27,7 @@ from oracle import adamw_oracle as O
 from shampoo_second_order_b200 import _lib as L
 
 U = 2.0 ** -24
+FLT_MAX = float(np.finfo(np.float32).max)
 B1, B2, EPS = 0.9, 0.999, 1e-8
 
 torch = pytest.importorskip("torch")
@@ -57,7 +58,7 @@ def test_oracle_codes_are_e4m3():
 
 
 def test_oracle_scale_is_the_smallest_that_fits():
-    x = np.array([[0.0], [448.0], [np.nextafter(448.0, 1e3)], [1e-45], [O.FLT_MAX], [1.75], [1.76]]) * np.ones((1, 256))
+    x = np.array([[0.0], [448.0], [np.nextafter(448.0, 1e3)], [1e-45], [FLT_MAX], [1.75], [1.76]]) * np.ones((1, 256))
     e = O.scale_bytes(x)
     assert list(e) == [1, 127, 128, 1, 247, 119, 120]
     for k in (1, 2, 4, 5, 6):
@@ -113,7 +114,7 @@ def lib():
     (dict(numel=[]), "nparams"), (dict(numel=[4, 0]), "element count"), (dict(numel=[1 << 41]), "element count"),
     (dict(numel=[1 << 40] * 20), "more elements"),
     (dict(beta1=1.0), "beta1"), (dict(beta1=-0.1), "beta1"), (dict(beta2=1.0), "beta2"), (dict(beta2=float("nan")), "beta"),
-    (dict(epsilon=0.0), "epsilon"), (dict(epsilon=1e-60), "epsilon"), (dict(epsilon=float("inf")), "epsilon"),
+    (dict(epsilon=0.0), "epsilon"), (dict(epsilon=1e-60), "epsilon"), (dict(epsilon=1e-39), "epsilon"), (dict(epsilon=float("inf")), "epsilon"),
     (dict(state_bits=16), "state_bits"), (dict(grad_dtype=7), "dtype"),
     (dict(max_norm=-1.0), "max_norm"), (dict(max_norm=float("nan")), "max_norm"),
     (dict(weight_decay=[-1.0]), "weight_decay"), (dict(weight_decay=[float("nan")]), "weight_decay"),
@@ -289,7 +290,7 @@ def check_step(opt, P, lr, decay, max_norm, seed, copies):
         # where v is in the subnormal range r has an absolute error of sqrt(its)
         er = (5 + gerr) * U * r + np.where(v < 1e-37, 2e-22, 0.0)
         ew = 1.01 * (U * (np.abs(w0[i]) + np.abs(w)) + first / d * em
-                     + first * np.abs(m) / d * (7 * U + er / math.sqrt(1 - B2 ** t) / d)) + 1e-45
+                     + first * np.abs(m) / d * (9 * U + er / math.sqrt(1 - B2 ** t) / d)) + 1e-45
         got = f64(P.w[i])
         assert (np.abs(got - w) <= ew).all(), (i, t, np.max(np.abs(got - w) / ew))
         if copies:   # the copy is this very weight, rounded to nearest
@@ -386,8 +387,8 @@ def test_adamw_skips_gradients_that_are_not_finite(cuda, state, gdt, value):
 @gpu
 @pytest.mark.parametrize("state", ["f32", "8bit"])
 def test_adamw_extreme_gradients(cuda, state):
-    """Squares beyond and below the range of a float, zeros, and the largest float: finite results, moments that
-    stop at the largest float, and a norm."""
+    """Squares beyond and below the range of a float, zeros, and the largest float: finite results, a norm, and beyond
+    2^63 the step of a gradient of 2^63."""
     from shampoo_second_order_b200 import AdamW
     for value in (1e25, 3.4028234663852886e38, 1e-25, 1e-38, 0.0):
         P = Params([1000, 300], "f32", seed=6)
@@ -398,11 +399,16 @@ def test_adamw_extreme_gradients(cuda, state):
         for t in range(3):
             opt.step(P.w, P.g, 1e-2)
             norm = value * math.sqrt(1300)
-            assert float(opt.grad_norm()) == pytest.approx(norm if norm < O.FLT_MAX else math.inf, rel=1e-6)
+            assert float(opt.grad_norm()) == pytest.approx(norm if norm < FLT_MAX else math.inf, rel=1e-6)
         for i, w in enumerate(P.w):
             assert np.isfinite(f64(w)).all() and np.isfinite(moments(opt, i)[0]).all() and np.isfinite(moments(opt, i)[1]).all()
             if value == 0.0:
                 assert np.array_equal(f64(w), w0[i])
+            if value > 2.0 ** 63 and state == "f32":
+                g = np.sign(f64(P.g[i])) * 2.0 ** 63
+                m, v = g * (1 - B1 ** 3), g * g * (1 - B2 ** 3)
+                assert (np.abs(moments(opt, i)[0] - m) <= 12 * U * np.abs(m)).all()
+                assert (np.abs(moments(opt, i)[1] - v) <= 18 * U * v).all()
 
 
 @gpu
