@@ -93,7 +93,7 @@ shampoo_status check_list(int nparams, const int64_t* numel, int grad_dtype) {
   for (int i = 0; i < nparams; ++i) {
     if (numel[i] < 1 || numel[i] > (int64_t(1) << 40))
       return refuse(nullptr, SHAMPOO_EINVAL, "bad element count for parameter " + std::to_string(i));
-    total += (numel[i] + kListChunk - 1) / kListChunk;
+    total += (numel[i] + kListChunk - 1) / kListChunk + 1;   // chunks
     if (total > (int64_t(1) << 30)) return refuse(nullptr, SHAMPOO_EINVAL, "more elements than a list can hold");
   }
   return SHAMPOO_OK;
@@ -109,13 +109,14 @@ shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dt
   for (int i = 0; i < nparams; ++i) {
     if (i % kListGroup == 0) l->groups.push_back(Group{i, 0, (int)chunks.size(), 0, 0});
     l->offset.push_back(l->total);
-    for (int64_t s = 0; s < numel[i]; s += kListChunk) {
+    for (int64_t s = 0; s < numel[i];) {
       ListChunk c{};
       c.param = i;
-      c.len = (int)std::min<int64_t>(kListChunk, numel[i] - s);
       c.start = s;
       c.flat = l->total + s;
+      c.len = (int)std::min<int64_t>(kListChunk - c.flat % kListChunk, numel[i] - s);
       chunks.push_back(c);
+      s += c.len;
     }
     l->total += (numel[i] + kQBlock - 1) / kQBlock * kQBlock;
     Group& g = l->groups.back();

@@ -11,11 +11,12 @@ constexpr int kListWarps = 8;      // warps per CTA of the list kernels
 constexpr int kQBlock = 256;       // elements per scale of the 8-bit moments; every
                                    // tensor's state starts at a multiple of it
 
-// A contiguous run of one tensor's elements, at most kListChunk of them.
+// A contiguous run of one tensor's elements that lies between two multiples of
+// kListChunk in the flat state (so that the scales of its blocks lie in one 32-byte sector).
 struct ListChunk {
   int param;
   int len;
-  int64_t start;   // first element inside the tensor, a multiple of kListChunk
+  int64_t start;   // first element inside the tensor, a multiple of kQBlock
   int64_t flat;    // first element in the flat state, a multiple of kQBlock
 };
 
