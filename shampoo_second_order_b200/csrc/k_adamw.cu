@@ -428,6 +428,7 @@ __device__ __forceinline__ F2 f2(float a, float b) {
   return o;
 }
 __device__ __forceinline__ F2 f2(float a) { return f2(a, a); }
+__device__ __forceinline__ F2 f2(float2 a) { return f2(a.x, a.y); }
 __device__ __forceinline__ float2 un2(F2 a) {
   float2 o;
   asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(a.v));
@@ -443,48 +444,91 @@ __device__ __forceinline__ F2 operator+(F2 a, F2 b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(o.v) : "l"(a.v), "l"(b.v));
   return o;
 }
+__device__ __forceinline__ F2 operator-(F2 a, F2 b) {
+  F2 o;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(o.v) : "l"(a.v), "l"(b.v));
+  return o;
+}
 __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   F2 o;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(o.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return o;
 }
-__device__ __forceinline__ F2 minus(F2 a, F2 b) { return fma2(b, f2(-1.0f), a); }   // exact as a - b
 
-__device__ __forceinline__ float lift_of(float a) { return a < 0x1p-6f ? 0x1p-6f : 0.0f; }
-__device__ __forceinline__ F2 masked(F2 a, uint32_t mask) {
-  const float2 x = un2(a);
-  return f2(__uint_as_float(__float_as_uint(x.x) & mask), __uint_as_float(__float_as_uint(x.y) & mask));
+// The codes are 2^-9 apart below 2^-6, throughout, as they are in [2^-6, 2^-5): values
+// there are lifted by 2^-6 for the rounding (LIFT: some value of the block lies below,
+// and is not zero).  1 where a < 2^-6, else 0: 2^30 (2^-6 - a), which is 1 or
+// more for the next float below 2^-6, cut to [0, 1].
+template <bool LIFT>
+__device__ __forceinline__ float below(float a) {
+  return LIFT ? __saturatef(fmaf(a, -0x1p30f, 0x1p24f)) : 0.0f;
+}
+template <bool LIFT>
+__device__ __forceinline__ float lifted(float a, float s, float by) {
+  return LIFT ? fmaf(s, by, a) : a;
 }
 
 // a in [0, 448] to a value of e4m3, up where the 16 random bits and the 20 bits
-// that are cut off carry.  Below 2^-6 the codes are 2^-9 apart throughout, as they
-// are in [2^-6, 2^-5): values there are lifted by 2^-6 for the rounding.
-__device__ __forceinline__ F2 round_m(float a0, float a1, uint32_t bits0, uint32_t bits1) {
-  const F2 lift = f2(lift_of(a0), lift_of(a1));
-  const float2 x = un2(f2(a0, a1) + lift);
-  const F2 y = f2(__uint_as_float((__float_as_uint(x.x) + (bits0 << 4)) & 0xFFF00000u),
-                  __uint_as_float((__float_as_uint(x.y) + (bits1 << 4)) & 0xFFF00000u));
-  return minus(y, lift);
+// that are cut off carry.
+template <bool LIFT>
+__device__ __forceinline__ float round_m(float a, uint32_t bits) {
+  const float s = below<LIFT>(a);
+  const uint32_t word = __float_as_uint(lifted<LIFT>(a, s, 0x1p-6f));
+  return lifted<LIFT>(__uint_as_float((word + bits * 16) & 0xFFF00000u), s, -0x1p-6f);
 }
-__device__ __forceinline__ F2 round_r(F2 a, uint32_t bits0, uint32_t bits1) {
-  const float2 s = un2(a);
-  const F2 lift = f2(lift_of(s.x), lift_of(s.y));
-  const F2 word = a + lift;
-  const F2 lo = minus(masked(word, 0xFFF00000u), lift);
-  const F2 gap = masked(word, 0x7F800000u) * f2(0.125f);
-  const F2 hi = lo + gap;
-  // bits / 2^16, from the significand of a number in [1, 2)
-  const F2 chance = f2(__uint_as_float(bits0 * 128 + 0x3F800000u), __uint_as_float(bits1 * 128 + 0x3F800000u)) + f2(-1.0f);
-  const float2 p = un2(minus(a, lo) * (a + lo)), q = un2(chance * (gap * (lo + hi)));
-  const float2 l = un2(lo), u = un2(hi);
-  return f2(p.x > q.x ? u.x : l.x, p.y > q.y ? u.y : l.y);
+// The same, up where (a^2 - lo^2) > bits / 2^16 (hi^2 - lo^2).
+template <bool LIFT>
+__device__ __forceinline__ F2 round_r(F2 a2, uint32_t bits0, uint32_t bits1) {
+  const float2 a = un2(a2);
+  const float s0 = below<LIFT>(a.x), s1 = below<LIFT>(a.y);
+  const uint32_t w0 = __float_as_uint(lifted<LIFT>(a.x, s0, 0x1p-6f)), w1 = __float_as_uint(lifted<LIFT>(a.y, s1, 0x1p-6f));
+  const float2 lo = make_float2(lifted<LIFT>(__uint_as_float(w0 & 0xFFF00000u), s0, -0x1p-6f),
+                                lifted<LIFT>(__uint_as_float(w1 & 0xFFF00000u), s1, -0x1p-6f));
+  // eight gaps between codes
+  const float2 gap8 = make_float2(__uint_as_float(w0 & 0x7F800000u), __uint_as_float(w1 & 0x7F800000u));
+  const float2 hi = make_float2(fmaf(gap8.x, 0.125f, lo.x), fmaf(gap8.y, 0.125f, lo.y));
+  // bits / 2^19, from the significand of a number in [1/8, 1/4)
+  const F2 chance = f2(__uint_as_float(bits0 * 128 + 0x3E000000u) - 0.125f, __uint_as_float(bits1 * 128 + 0x3E000000u) - 0.125f);
+  const float2 p = un2((a2 - f2(lo)) * (a2 + f2(lo))), q = un2(chance * (f2(gap8) * (f2(lo) + f2(hi))));
+  return f2(p.x > q.x ? hi.x : lo.x, p.y > q.y ? hi.y : lo.y);
+}
+
+// The moments of a lane, m and r, to e4m3 values: im, ir are the scales' reciprocals.
+// first: what the lane's first element is hashed from, at(q) the q-th's distance from it.
+template <bool LIFT, class At>
+__device__ __forceinline__ void round_block(F2 (&m)[4], F2 (&r)[4], float im, float ir, uint32_t first, At at) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t h0 = mix32(first + (uint32_t)at(2 * k) * 0x9E3779B1u);
+    const uint32_t h1 = mix32(first + (uint32_t)at(2 * k + 1) * 0x9E3779B1u);
+    const float2 x = un2(m[k]);
+    m[k] = f2(copysignf(round_m<LIFT>(fabsf(x.x) * im, h0 & 0xFFFFu), x.x),
+              copysignf(round_m<LIFT>(fabsf(x.y) * im, h1 & 0xFFFFu), x.y));
+    r[k] = round_r<LIFT>(r[k] * f2(ir), h0 >> 16, h1 >> 16);
+  }
+}
+
+__device__ __forceinline__ float reciprocal(float x) {   // within one unit in the last place; x is normal
+  float o;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(x));
+  return o;
+}
+__device__ __forceinline__ float largest(float a, F2 b) {   // of three magnitudes
+  const float2 x = un2(b);
+  float o;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(o) : "f"(a), "f"(x.x), "f"(x.y));
+  return o;
+}
+__device__ __forceinline__ float smallest(float a, F2 b) {
+  const float2 x = un2(b);
+  float o;
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(o) : "f"(a), "f"(x.x), "f"(x.y));
+  return o;
 }
 
 // Loads that stay where they are written: all of a block's before the arithmetic.
-__device__ __forceinline__ uint4 ld16(const void* p) {
-  uint4 o;
-  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w) : "l"(p));
-  return o;
+__device__ __forceinline__ void ld16(const void* p, F2& a, F2& b) {
+  asm volatile("ld.global.v2.b64 {%0, %1}, [%2];" : "=l"(a.v), "=l"(b.v) : "l"(p));
 }
 __device__ __forceinline__ uint2 ld8(const void* p) {
   uint2 o;
@@ -496,15 +540,21 @@ __device__ __forceinline__ uint32_t ld4(const void* p) {
   asm volatile("ld.global.b32 %0, [%1];" : "=r"(o) : "l"(p));
   return o;
 }
-// Codes to floats and back; values of e4m3 convert exactly.
-__device__ __forceinline__ float2 code_values(uint32_t two) {
-  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
+
+// Two codes to floats and back; values of e4m3 convert exactly.
+__device__ __forceinline__ F2 code_values(uint32_t two) {
+  return f2(__half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3))));
 }
-__device__ __forceinline__ uint32_t value_codes(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t value_codes(F2 a) {
+  return __nv_cvt_float2_to_fp8x2(un2(a), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t bf16_pair(F2 a) {
+  const float2 x = un2(a);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One warp steps one block: eight elements a lane.  Whole: the block is full and
+// One warp steps one block: four pairs of elements a lane.  Whole: the block is full and
 // the pointers are aligned to four elements; lane l holds elements 4l..4l+3 of
 // either half.  Otherwise element 32 q + l is lane l's q-th, so that accesses of single elements
 // are those of neighbouring lanes to neighbouring addresses.
@@ -517,137 +567,119 @@ __device__ __forceinline__ void step_block(const Update& u, int o, const AdamwSt
   const auto at = [&](int q) { return WHOLE ? 128 * (q >> 2) + 4 * lane + (q & 3) : 32 * q + lane; };
   const auto in = [&](int q) { return WHOLE || o + at(q) < u.c.len; };
   uint8_t *mq = st.mq + flat, *rq = st.rq + flat;
-  float* w = u.w + o;
-  float xw[8], xg[8], m[8], r[8];
+  float* wp = u.w + o;
+  F2 w[4], g[4], m[4], r[4];
   if (WHOLE) {
     uint32_t cm[2], cr[2];
-    uint4 lw[2], lg[2];
-    const char* g = static_cast<const char*>(u.g) + (u.c.start + o) * (BF16 ? 2 : 4);
+    uint2 cg[2];
+    const char* gp = static_cast<const char*>(u.g) + (u.c.start + o) * (BF16 ? 2 : 4);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = 128 * k + 4 * lane;
       cm[k] = ld4(mq + i);
       cr[k] = ld4(rq + i);
-      lw[k] = ld16(w + i);
-      if (BF16) {
-        const uint2 two = ld8(g + 2 * i);
-        lg[k].x = two.x;
-        lg[k].y = two.y;
-      } else {
-        lg[k] = ld16(g + 4 * i);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t a[4] = {lw[k].x, lw[k].y, lw[k].z, lw[k].w}, b[4] = {lg[k].x, lg[k].y, lg[k].z, lg[k].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        xw[4 * k + q] = __uint_as_float(a[q]);
-        xg[4 * k + q] = __uint_as_float(BF16 ? (q & 1 ? b[q >> 1] & 0xFFFF0000u : b[q >> 1] << 16) : b[q]);
-      }
+      if (BF16) cg[k] = ld8(gp + 2 * i);
+      else ld16(gp + 4 * i, g[2 * k], g[2 * k + 1]);
+      ld16(wp + i, w[2 * k], w[2 * k + 1]);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 a = code_values(cm[k >> 1] >> (16 * (k & 1))), b = code_values(cr[k >> 1] >> (16 * (k & 1)));
-      m[2 * k] = a.x;
-      m[2 * k + 1] = a.y;
-      r[2 * k] = b.x;
-      r[2 * k + 1] = b.y;
+      m[k] = code_values(cm[k >> 1] >> (16 * (k & 1)));
+      r[k] = code_values(cr[k >> 1] >> (16 * (k & 1)));
+      if (BF16) {
+        const uint32_t two = k & 1 ? cg[k >> 1].y : cg[k >> 1].x;
+        g[k] = f2(__uint_as_float(two << 16), __uint_as_float(two & 0xFFFF0000u));
+      }
     }
   } else {
-    uint8_t cm[8], cr[8];
+    float xw[8], xg[8];
+    uint32_t cm[8], cr[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      xw[q] = in(q) ? w[at(q)] : 0.0f;
+      xw[q] = in(q) ? wp[at(q)] : 0.0f;
       xg[q] = in(q) ? load1<BF16>(u.g, u.c.start + o + at(q)) : 0.0f;
       cm[q] = mq[at(q)];
       cr[q] = rq[at(q)];
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      m[q] = code_values(cm[q]).x;
-      r[q] = code_values(cr[q]).x;
+    for (int k = 0; k < 4; ++k) {
+      w[k] = f2(xw[2 * k], xw[2 * k + 1]);
+      g[k] = f2(xg[2 * k], xg[2 * k + 1]);
+      m[k] = code_values(cm[2 * k] | (cm[2 * k + 1] << 8));
+      r[k] = code_values(cr[2 * k] | (cr[2 * k + 1] << 8));
     }
   }
-  const float ms = scale_of(em), rs = scale_of(er);
   // b1 (code * scale) is (b1 scale) code: the scale is a power of two
-  const F2 b1ms = f2(h.beta1 * ms), rs2 = f2(rs);
-  float mm = 0.0f, rm = 0.0f;
+  const F2 b1ms = f2(h.beta1 * scale_of(em)), rs = f2(scale_of(er));
 #pragma unroll
-  for (int k = 0; k < 8; k += 2) {
-    F2 g = f2(xg[k], xg[k + 1]) * f2(u.coef);
-    if (u.huge) {
-      const float2 x = un2(g);
-      g = f2(limit(x.x), limit(x.y));
+  for (int k = 0; k < 4; ++k) g[k] = g[k] * f2(u.coef);
+  if (u.huge) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = un2(g[k]);
+      g[k] = f2(limit(x.x), limit(x.y));
     }
-    const float2 xm = un2(f2(m[k], m[k + 1]) * b1ms + f2(h.omb1) * g);
-    const F2 r0 = f2(r[k], r[k + 1]) * rs2;
-    const float2 v = un2(f2(h.beta2) * (r0 * r0) + f2(h.omb2) * g * g);
-    m[k] = xm.x;
-    m[k + 1] = xm.y;
-    r[k] = sqrtf(v.x);
-    r[k + 1] = sqrtf(v.y);
-    const float2 d = un2(fma2(f2(r[k], r[k + 1]), f2(u.s.second), f2(h.eps)));
-    const F2 move = f2(-u.s.first) * f2(__fdividef(xm.x, d.x), __fdividef(xm.y, d.y));
-    const float2 x = un2(fma2(f2(xw[k], xw[k + 1]), f2(u.s.shrink), move));
-    xw[k] = x.x;
-    xw[k + 1] = x.y;
-    mm = fmaxf(mm, fmaxf(fabsf(xm.x), fabsf(xm.y)));
-    rm = fmaxf(rm, fmaxf(r[k], r[k + 1]));
+  }
+  float mm = 0.0f, vm = 0.0f, ml = FLT_MAX, rl = FLT_MAX;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    m[k] = m[k] * b1ms + f2(h.omb1) * g[k];
+    r[k] = r[k] * rs;
+    const F2 v = f2(h.beta2) * (r[k] * r[k]) + f2(h.omb2) * g[k] * g[k];
+    mm = largest(mm, m[k]);
+    vm = largest(vm, v);
+    const float2 x = un2(v);
+    r[k] = f2(sqrtf(x.x), sqrtf(x.y));
+    ml = smallest(ml, m[k]);
+    rl = smallest(rl, r[k]);
+    const float2 d = un2(fma2(r[k], f2(u.s.second), f2(h.eps)));
+    w[k] = fma2(w[k], f2(u.s.shrink), m[k] * f2(reciprocal(d.x), reciprocal(d.y)) * f2(-u.s.first));
   }
   if (WHOLE) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = 128 * k + 4 * lane;
-      store4<false>(w, i, *reinterpret_cast<const float(*)[4]>(xw + 4 * k));
-      if (u.b) *reinterpret_cast<uint2*>(u.b + o + i) = bf16_bits4(xw + 4 * k);
+      *reinterpret_cast<ulonglong2*>(wp + i) = make_ulonglong2(w[2 * k].v, w[2 * k + 1].v);
+      if (u.b) *reinterpret_cast<uint2*>(u.b + o + i) = make_uint2(bf16_pair(w[2 * k]), bf16_pair(w[2 * k + 1]));
     }
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       if (!in(q)) continue;
-      w[at(q)] = xw[q];
-      if (u.b) u.b[o + at(q)] = bf16_bits(xw[q]);
+      const float2 two = un2(w[q >> 1]);
+      const float x = q & 1 ? two.y : two.x;
+      wp[at(q)] = x;
+      if (u.b) u.b[o + at(q)] = bf16_bits(x);
     }
   }
-  // magnitudes order as their bits do
+  // magnitudes order as their bits do, and roots as their squares
   em = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(mm)));
-  er = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(rm)));
-  const float im = inverse_scale(em);
-  const F2 ir = f2(inverse_scale(er));
+  er = scale_byte(__float_as_uint(sqrtf(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm))))));
+  const float im = inverse_scale(em), ir = inverse_scale(er);
   const uint32_t base = (uint32_t)flat * 0x9E3779B1u + (uint32_t)(flat >> 32) * 0x85EBCA77u + u.s.key;
-  const uint32_t lane_base = base + (uint32_t)at(0) * 0x9E3779B1u;
-#pragma unroll
-  for (int k = 0; k < 8; k += 2) {
-    const uint32_t h0 = mix32(lane_base + (uint32_t)(at(k) - at(0)) * 0x9E3779B1u);
-    const uint32_t h1 = mix32(lane_base + (uint32_t)(at(k + 1) - at(0)) * 0x9E3779B1u);
-    const float2 x = un2(round_m(fabsf(m[k] * im), fabsf(m[k + 1] * im), h0 & 0xFFFFu, h1 & 0xFFFFu));
-    m[k] = copysignf(x.x, m[k]);
-    m[k + 1] = copysignf(x.y, m[k + 1]);
-    const float2 y = un2(round_r(f2(r[k], r[k + 1]) * ir, h0 >> 16, h1 >> 16));
-    r[k] = y.x;
-    r[k + 1] = y.y;
-  }
+  const uint32_t first = base + (uint32_t)at(0) * 0x9E3779B1u;
+  const auto from = [&](int q) { return WHOLE ? 128 * (q >> 2) + (q & 3) : 32 * q; };
+  // an element 2^15 below the block's largest: hardly ever, but for zeros
+  if (__any_sync(0xffffffffu, fminf(ml * im, rl * ir) < 0x1p-6f)) round_block<true>(m, r, im, ir, first, from);
+  else round_block<false>(m, r, im, ir, first, from);
   if (WHOLE) {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = 128 * k + 4 * lane;
-      *reinterpret_cast<uint32_t*>(mq + i) =
-          value_codes(m[4 * k], m[4 * k + 1]) | (value_codes(m[4 * k + 2], m[4 * k + 3]) << 16);
-      *reinterpret_cast<uint32_t*>(rq + i) =
-          value_codes(r[4 * k], r[4 * k + 1]) | (value_codes(r[4 * k + 2], r[4 * k + 3]) << 16);
+      *reinterpret_cast<uint32_t*>(mq + i) = value_codes(m[2 * k]) | (value_codes(m[2 * k + 1]) << 16);
+      *reinterpret_cast<uint32_t*>(rq + i) = value_codes(r[2 * k]) | (value_codes(r[2 * k + 1]) << 16);
     }
   } else {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {   // behind the tensor's end: zeros, as they were
-      mq[at(q)] = (uint8_t)value_codes(m[q], 0.0f);
-      rq[at(q)] = (uint8_t)value_codes(r[q], 0.0f);
+      mq[at(q)] = (uint8_t)(value_codes(m[q >> 1]) >> (8 * (q & 1)));
+      rq[at(q)] = (uint8_t)(value_codes(r[q >> 1]) >> (8 * (q & 1)));
     }
   }
 }
 
 template <bool BF16, int K>
-__global__ void __launch_bounds__(kThreads, 3) adamw_8bit_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
+__global__ void __launch_bounds__(kThreads, 4) adamw_8bit_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
                                                                  const __grid_constant__ Pointers<K> gp,
                                                                  const __grid_constant__ Pointers<K> cp, int copies,
                                                                  int p0, int c0, AdamwState st,
