@@ -11,6 +11,7 @@
 
 #include <type_traits>
 
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -29,6 +30,11 @@ template <int K>
 struct Pointers {
   const void* p[K];
 };
+
+// The kernels after the gradient pass start while it runs: they fetch what does not
+// depend on it, then wait for its end.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ---------------- element access ----------------
 
@@ -129,15 +135,25 @@ __device__ __forceinline__ void widen(const uint4& u, float* x) {
   }
 }
 
+// b^n by squaring, off by at most about n roundings of 64 bits.
+__device__ __forceinline__ double power(double b, unsigned n) {
+  double r = 1.0;
+  for (; n; n >>= 1) {
+    if (n & 1) r *= b;
+    b *= b;
+  }
+  return r;
+}
+
 // One tensor's factors of the step that it takes if its gradient is finite.
 // 1 - b^t loses digits where t is small: in 64 bits, rounded once.
 __device__ void step_factors(const ListAdvance& adv, int p) {
-  const int n = adv.step[p] + 1;
+  const unsigned n = (unsigned)adv.step[p] + 1;
   ListStep o;
-  o.first = (float)(adv.lr / (1.0 - pow(adv.beta1, (double)n)));
-  o.second = (float)(1.0 / sqrt(1.0 - pow(adv.beta2, (double)n)));
+  o.first = (float)(adv.lr / (1.0 - power(adv.beta1, n)));
+  o.second = (float)(1.0 / sqrt(1.0 - power(adv.beta2, n)));
   o.shrink = (float)(1.0 - adv.lr * adv.decay[p]);
-  o.key = mix32(adv.seed_lo + mix32(adv.seed_hi) + (uint32_t)n * 0x632BE5ABu);
+  o.key = mix32(adv.seed_lo + mix32(adv.seed_hi) + n * 0x632BE5ABu);
   adv.out[p] = o;
 }
 
@@ -157,8 +173,11 @@ __device__ void close_pass(const ListTables& t, unsigned pass, double max_norm, 
   if (__ldcg(&t.result->bad) != pass) {
     for (int b = threadIdx.x; b < t.nctas; b += blockDim.x) sum += __ldcg(&t.csum[b]);
   } else {   // without the skipped tensors' chunks
-    for (int i = threadIdx.x; i < t.nchunks * kListWarps; i += blockDim.x)
-      if (!t.skip[t.chunks[i / kListWarps].param]) sum += __ldcg(&t.partial[i]);
+#pragma unroll 8
+    for (int i = threadIdx.x; i < t.nchunks; i += blockDim.x) {
+      const double x = __ldcg(&t.partial[i]);
+      sum += t.skip[t.chunks[i].param] ? 0.0 : x;
+    }
   }
   sum = block_sum(sum, red);
   const double all = block_sum((double)skipped, red);
@@ -177,10 +196,11 @@ __device__ void close_pass(const ListTables& t, unsigned pass, double max_norm, 
 // below the normal range, is gone through again in 64 bits; that also finds the
 // elements that are not finite.
 //
-// A CTA walks over many chunks with all of a thread's loads of a chunk in
-// flight at once, and its warps join their sums once, at the end.  (A CTA a chunk spent
-// most of its life in the joining: 167 us for 285M bfloat16 elements.)  The sums of each
-// warp's part of a chunk are kept for the case that a tensor has to be left out.
+// A CTA walks over a range of chunks with all of a thread's loads of a chunk in flight
+// at once, and joins its threads' sums where the tensor changes.  (A CTA a chunk
+// spent most of its life in the joining: 167 us for 285M bfloat16 elements.)  The
+// sum up to there is kept with the run's last chunk, for the case that a tensor
+// has to be left out.
 template <bool BF16, int K>
 __global__ void __launch_bounds__(kThreads, 4) list_norm_kernel(ListTables t, const __grid_constant__ Pointers<K> ptr,
                                                                 int p0, int np, int c0, int nc, int b0, double max_norm,
@@ -188,12 +208,15 @@ __global__ void __launch_bounds__(kThreads, 4) list_norm_kernel(ListTables t, co
   using V = Vectors<BF16>;
   __shared__ double red[kListWarps];
   __shared__ bool last;
+  let_next_start();
   const unsigned pass = t.result->pass;
-  if (adv.step)
-    for (int p = blockIdx.x * kThreads + threadIdx.x; p < np; p += gridDim.x * kThreads) step_factors(adv, p0 + p);
-  double total = 0.0;
-  for (int i = blockIdx.x; i < nc; i += gridDim.x) {
-    const ListChunk c = t.chunks[c0 + i];
+  const int i0 = c0 + (int)((int64_t)nc * blockIdx.x / gridDim.x);
+  const int i1 = c0 + (int)((int64_t)nc * (blockIdx.x + 1) / gridDim.x);
+  double total = 0.0, sum = 0.0;
+  bool bad = false;
+  ListChunk next = t.chunks[i0];
+  for (int i = i0; i < i1; ++i) {
+    const ListChunk c = next;
     const V vec(ptr.p[c.param - p0], c.start, c.len);
     uint4 u[V::N];
 #pragma unroll
@@ -201,12 +224,11 @@ __global__ void __launch_bounds__(kThreads, 4) list_norm_kernel(ListTables t, co
       const int v = threadIdx.x + k * kThreads;
       u[k] = v < vec.nvec ? *vec.at(v) : make_uint4(0, 0, 0, 0);
     }
-    double sum = 0.0;
-    bool bad = false;
+    if (i + 1 < i1) next = t.chunks[i + 1];
     if (const void* one = vec.single()) {
       const float x = load1<BF16>(one, 0);
-      bad = !isfinite(x);
-      sum = (double)x * x;
+      bad |= !isfinite(x);
+      sum += (double)x * x;
     }
     constexpr int G = 16 / V::E;   // vectors of sixteen elements
 #pragma unroll
@@ -227,17 +249,26 @@ __global__ void __launch_bounds__(kThreads, 4) list_norm_kernel(ListTables t, co
         }
       }
     }
-    sum = warp_sum(sum);
-    if (__any_sync(0xffffffffu, bad) && (threadIdx.x & 31) == 0) t.mark[c.param] = t.result->bad = pass;
-    if ((threadIdx.x & 31) == 0) t.partial[(int64_t)(c0 + i) * kListWarps + (threadIdx.x >> 5)] = sum;
-    total += sum;
+    const bool ends = i + 1 == i1 || next.param != c.param;
+    if (ends) {
+      sum = block_sum(sum, red);
+      const bool any = __syncthreads_or(bad);
+      if (threadIdx.x == 0) {
+        total += sum;
+        if (any) t.mark[c.param] = t.result->bad = pass;
+      }
+    }
+    if (threadIdx.x == 0) t.partial[i] = ends ? sum : 0.0;
+    if (ends) {
+      sum = 0.0;
+      bad = false;
+    }
   }
-  // every lane of a warp holds its warp's total
-  const double sum = block_sum((threadIdx.x & 31) == 0 ? total : 0.0, red);
-  __threadfence();
+  if (adv.step)
+    for (int p = blockIdx.x * kThreads + threadIdx.x; p < np; p += gridDim.x * kThreads) step_factors(adv, p0 + p);
   __syncthreads();
   if (threadIdx.x == 0) {
-    t.csum[b0 + blockIdx.x] = sum;
+    t.csum[b0 + blockIdx.x] = total;
     __threadfence();
     last = atomicAdd(&t.result->done, 1u) == (unsigned)t.nctas - 1;
   }
@@ -252,11 +283,11 @@ template <bool BF16, int K>
 __global__ void __launch_bounds__(kThreads) list_scale_kernel(ListTables t, const __grid_constant__ Pointers<K> ptr,
                                                               int p0, int c0) {
   using V = Vectors<BF16>;
-  const float coef = t.result->coef;
-  if (coef == 1.0f) return;
   const ListChunk c = t.chunks[c0 + gridDim.x - 1 - blockIdx.x];
-  if (t.skip[c.param]) return;
   const V vec(ptr.p[c.param - p0], c.start, c.len);
+  wait_for_previous();
+  const float coef = t.result->coef;
+  if (coef == 1.0f || t.skip[c.param]) return;
   uint4 u[V::N];
 #pragma unroll
   for (int k = 0; k < V::N; ++k) {
@@ -288,135 +319,6 @@ __global__ void __launch_bounds__(kThreads) list_scale_kernel(ListTables t, cons
 }
 
 // ---------------- AdamW ----------------
-
-struct Hyper {
-  float beta1, omb1, beta2, omb2, eps;
-};
-
-// What a CTA of the update needs to know of its chunk.
-struct Update {
-  ListChunk c;
-  ListStep s;
-  float coef;
-  bool huge;       // a gradient element may have a square beyond the largest float
-  float* w;
-  const void* g;
-  uint16_t* b;     // the bfloat16 copy, or null
-};
-
-// The chunks in the reverse of the norm's order: the gradients that it read last
-// are still in L2.  False where the tensor is skipped.
-template <int K>
-__device__ __forceinline__ bool update_of(Update& u, const ListTables& t, const Pointers<K>& wp, const Pointers<K>& gp,
-                                          const Pointers<K>& cp, int copies, int p0, int c0, const ListStep* step) {
-  u.c = t.chunks[c0 + gridDim.x - 1 - blockIdx.x];
-  if (t.skip[u.c.param]) return false;
-  u.s = step[u.c.param];
-  u.coef = t.result->coef;
-  u.huge = !(t.result->norm * u.coef < kGradMax);   // no element exceeds the norm
-  u.w = static_cast<float*>(const_cast<void*>(wp.p[u.c.param - p0])) + u.c.start;
-  u.g = gp.p[u.c.param - p0];
-  u.b = copies ? static_cast<uint16_t*>(const_cast<void*>(cp.p[u.c.param - p0])) + u.c.start : nullptr;
-  return true;
-}
-
-__device__ __forceinline__ float limit(float g) { return fminf(fmaxf(g, -kGradMax), kGradMax); }
-
-// Products and sums of the moments are rounded one by one, as written: left to the
-// compiler to fuse, a last bit that came out differently in another build would round
-// to another 8-bit code.
-__device__ __forceinline__ float next_m(float b1m, float g, const Hyper& h) {
-  return __fadd_rn(b1m, __fmul_rn(h.omb1, g));
-}
-__device__ __forceinline__ float next_v(float b2v, float g, const Hyper& h) {
-  return __fadd_rn(b2v, __fmul_rn(__fmul_rn(h.omb2, g), g));
-}
-// The quotient by the fast reciprocal: 2 units in the last place of a term that moves
-// the weight by about lr.
-__device__ __forceinline__ float next_w(float w, float m, float r, const ListStep& s, const Hyper& h) {
-  return fmaf(w, s.shrink, -s.first * __fdividef(m, fmaf(r, s.second, h.eps)));
-}
-
-__device__ __forceinline__ uint16_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
-__device__ __forceinline__ uint2 bf16_bits4(const float* x) {
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-}
-
-// One thread steps four elements at a time where the tensor's pointers are aligned to
-// four, and single ones, neighbouring threads neighbouring elements, where not.
-template <bool BF16, int K>
-__global__ void __launch_bounds__(kThreads) adamw_f32_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
-                                                             const __grid_constant__ Pointers<K> gp,
-                                                             const __grid_constant__ Pointers<K> cp, int copies,
-                                                             int p0, int c0, AdamwState st,
-                                                             const ListStep* __restrict__ step, Hyper h) {
-  Update u;
-  if (!update_of(u, t, wp, gp, cp, copies, p0, c0, step)) return;
-  float *m = st.m + u.c.flat, *v = st.v + u.c.flat;
-  int done = 0;
-  if (aligned4<false>(u.w) && aligned4<BF16>(u.g) && aligned4<true>(u.b)) {
-    done = u.c.len & ~3;
-#pragma unroll 2
-    for (int i = threadIdx.x * 4; i < done; i += 4 * kThreads) {
-      float xw[4], xg[4], xm[4], xv[4];
-      load4<false>(u.w, i, xw);
-      load4<BF16>(u.g, u.c.start + i, xg);
-      load4<false>(m, i, xm);
-      load4<false>(v, i, xv);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float g = __fmul_rn(xg[q], u.coef);
-        if (u.huge) g = limit(g);
-        xm[q] = next_m(__fmul_rn(h.beta1, xm[q]), g, h);
-        xv[q] = next_v(__fmul_rn(h.beta2, xv[q]), g, h);
-        xw[q] = next_w(xw[q], xm[q], sqrtf(xv[q]), u.s, h);
-      }
-      store4<false>(u.w, i, xw);
-      store4<false>(m, i, xm);
-      store4<false>(v, i, xv);
-      if (u.b) *reinterpret_cast<uint2*>(u.b + i) = bf16_bits4(xw);
-    }
-  }
-#pragma unroll 4
-  for (int i = done + threadIdx.x; i < u.c.len; i += kThreads) {
-    float g = __fmul_rn(load1<BF16>(u.g, u.c.start + i), u.coef);
-    if (u.huge) g = limit(g);
-    const float xm = next_m(__fmul_rn(h.beta1, m[i]), g, h);
-    const float xv = next_v(__fmul_rn(h.beta2, v[i]), g, h);
-    const float xw = next_w(u.w[i], xm, sqrtf(xv), u.s, h);
-    u.w[i] = xw;
-    m[i] = xm;
-    v[i] = xv;
-    if (u.b) u.b[i] = bf16_bits(xw);
-  }
-}
-
-// ---------------- 8-bit moments ----------------
-//
-// A block of 256 elements keeps m, and r = sqrt(v), as e4m3 codes times a
-// power of two, 2^(E - 127) with one byte E a block: the smallest that brings the
-// block's largest magnitude to 448, the largest code.  v itself would need twice
-// the exponent range that e4m3 has.
-//
-// The codes are rounded at random.  With b2 = 0.999 v moves by a tenth of a
-// percent a step and codes are 6 to 12 % apart: rounding to nearest would leave
-// nearly every code where it is, up to a hundredfold below g^2.  m goes up
-// with the probability of its fraction, which keeps its mean.  r goes up with the
-// probability (v - lo^2) / (hi^2 - lo^2), which keeps the mean of v: the fraction of
-// r would add the variance of each rounding to v, step after step.  Scales
-// are powers of two because then a value that has not changed is a code still
-// when the scale changes: only the change itself is rounded.
-
-// E of the scale: 448 = 1.75 * 2^8, so the exponent of the largest magnitude
-// less 8, and one more where its significand exceeds 1.75.
-__device__ __forceinline__ int scale_byte(uint32_t largest_bits) {
-  return max((int)((largest_bits + 0x1FFFFFu) >> 23) - 8, 1);
-}
-// 2^(E - 127), zero for the byte 0 of a fresh state
-__device__ __forceinline__ float scale_of(int e) { return __uint_as_float((uint32_t)e << 23); }
-// its reciprocal 2^(127 - E)
-__device__ __forceinline__ float inverse_scale(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
 
 // Two floats that the packed instructions of sm_100 work on, each rounded as alone.
 struct F2 {
@@ -454,6 +356,169 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(o.v) : "l"(a.v), "l"(b.v), "l"(c.v));
   return o;
 }
+
+struct Hyper {
+  float beta1, omb1, beta2, omb2, eps;
+  float2 omb1_2, beta2_2, omb2_2, eps_2;   // twice each, as the packed instructions read them
+};
+__host__ Hyper hyper(float beta1, float omb1, float beta2, float omb2, float eps) {
+  return Hyper{beta1, omb1, beta2, omb2, eps, {omb1, omb1}, {beta2, beta2}, {omb2, omb2}, {eps, eps}};
+}
+
+// What a CTA of the update needs to know of its chunk.
+struct Update {
+  ListChunk c;
+  float* w;
+  const char* g;
+  uint16_t* b;     // the bfloat16 copy, or null
+  bool aligned;    // all three to four elements
+  // what the gradient pass leaves
+  ListStep s;
+  float coef;
+  bool huge;       // a gradient element may have a square beyond the largest float
+};
+
+// The chunks in the reverse of the norm's order: the gradients that it read last
+// are still in L2.
+template <bool BF16, int K>
+__device__ __forceinline__ void update_of(Update& u, const ListTables& t, const Pointers<K>& wp, const Pointers<K>& gp,
+                                          const Pointers<K>& cp, int copies, int p0, int c0) {
+  u.c = t.chunks[c0 + gridDim.x - 1 - blockIdx.x];
+  u.w = static_cast<float*>(const_cast<void*>(wp.p[u.c.param - p0])) + u.c.start;
+  u.g = static_cast<const char*>(gp.p[u.c.param - p0]) + u.c.start * (BF16 ? 2 : 4);
+  u.b = copies ? static_cast<uint16_t*>(const_cast<void*>(cp.p[u.c.param - p0])) + u.c.start : nullptr;
+  u.aligned = aligned4<false>(u.w) && aligned4<BF16>(u.g) && aligned4<true>(u.b);
+}
+
+// Waits for the gradient pass; false where the tensor is skipped.
+__device__ __forceinline__ bool pass_results(Update& u, const ListTables& t, const ListStep* step) {
+  wait_for_previous();
+  const int skip = t.skip[u.c.param];
+  u.s = step[u.c.param];
+  u.coef = t.result->coef;
+  u.huge = !(t.result->norm * u.coef < kGradMax);   // no element exceeds the norm
+  return !skip;
+}
+
+__device__ __forceinline__ float limit(float g) { return fminf(fmaxf(g, -kGradMax), kGradMax); }
+
+// Products and sums of the moments are rounded one by one, as written: left to the
+// compiler to fuse, a last bit that came out differently in another build would round
+// to another 8-bit code.
+__device__ __forceinline__ float next_m(float b1m, float g, const Hyper& h) {
+  return __fadd_rn(b1m, __fmul_rn(h.omb1, g));
+}
+__device__ __forceinline__ float next_v(float b2v, float g, const Hyper& h) {
+  return __fadd_rn(b2v, __fmul_rn(__fmul_rn(h.omb2, g), g));
+}
+// The quotient by the fast reciprocal: 2 units in the last place of a term that moves
+// the weight by about lr.
+__device__ __forceinline__ float next_w(float w, float m, float r, const ListStep& s, const Hyper& h) {
+  return fmaf(w, s.shrink, -s.first * __fdividef(m, fmaf(r, s.second, h.eps)));
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ uint2 bf16_bits4(const float* x) {
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// Four elements of each array, as they are loaded.
+template <bool BF16>
+struct Four {
+  float w[4], g[4], m[4], v[4];
+  __device__ __forceinline__ void load(const Update& u, const float* mp, const float* vp, int i) {
+    load4<false>(u.w, i, w);
+    load4<BF16>(u.g, i, g);
+    load4<false>(mp, i, m);
+    load4<false>(vp, i, v);
+  }
+  __device__ __forceinline__ void step(const Update& u, float* mp, float* vp, int i, const Hyper& h) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      g[q] = __fmul_rn(g[q], u.coef);
+      if (u.huge) g[q] = limit(g[q]);
+      m[q] = next_m(__fmul_rn(h.beta1, m[q]), g[q], h);
+      v[q] = next_v(__fmul_rn(h.beta2, v[q]), g[q], h);
+      w[q] = next_w(w[q], m[q], sqrtf(v[q]), u.s, h);
+    }
+    store4<false>(u.w, i, w);
+    store4<false>(mp, i, m);
+    store4<false>(vp, i, v);
+    if (u.b) *reinterpret_cast<uint2*>(u.b + i) = bf16_bits4(w);
+  }
+};
+
+// Steps a run of a tensor: four elements a thread at a time where its pointers are
+// aligned to four, and single ones, neighbouring threads neighbouring elements, where not.
+// mp, vp: its moments; thread, threads: of those that step it together.
+// ready(): whether to go on, asked after the first loads.
+template <bool BF16, class Ready>
+__device__ __forceinline__ void step_run(Update& u, float* mp, float* vp, int thread, int threads, const Hyper& h,
+                                         Ready ready) {
+  const int whole = u.aligned ? u.c.len & ~3 : 0;
+  Four<BF16> a, b;
+  const int first = thread * 4, stride = 4 * threads;
+  if (first < whole) a.load(u, mp, vp, first);
+  if (first + stride < whole) b.load(u, mp, vp, first + stride);
+  if (!ready()) return;
+  for (int i = first; i < whole; i += 2 * stride) {
+    a.step(u, mp, vp, i, h);
+    if (i + 2 * stride < whole) a.load(u, mp, vp, i + 2 * stride);
+    if (i + stride >= whole) break;
+    b.step(u, mp, vp, i + stride, h);
+    if (i + 3 * stride < whole) b.load(u, mp, vp, i + 3 * stride);
+  }
+#pragma unroll 4
+  for (int i = whole + thread; i < u.c.len; i += threads) {
+    float g = __fmul_rn(load1<BF16>(u.g, i), u.coef);
+    if (u.huge) g = limit(g);
+    const float m = next_m(__fmul_rn(h.beta1, mp[i]), g, h);
+    const float v = next_v(__fmul_rn(h.beta2, vp[i]), g, h);
+    const float w = next_w(u.w[i], m, sqrtf(v), u.s, h);
+    u.w[i] = w;
+    mp[i] = m;
+    vp[i] = v;
+    if (u.b) u.b[i] = bf16_bits(w);
+  }
+}
+
+template <bool BF16, int K>
+__global__ void __launch_bounds__(kThreads) adamw_f32_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
+                                                             const __grid_constant__ Pointers<K> gp,
+                                                             const __grid_constant__ Pointers<K> cp, int copies,
+                                                             int p0, int c0, AdamwState st,
+                                                             const ListStep* step, Hyper h) {
+  Update u;
+  update_of<BF16>(u, t, wp, gp, cp, copies, p0, c0);
+  step_run<BF16>(u, st.m + u.c.flat, st.v + u.c.flat, threadIdx.x, kThreads, h, [&] { return pass_results(u, t, step); });
+}
+
+// ---------------- 8-bit moments ----------------
+//
+// A block of 256 elements keeps m, and r = sqrt(v), as e4m3 codes times a
+// power of two, 2^(E - 127) with one byte E a block: the smallest that brings the
+// block's largest magnitude to 448, the largest code.  v itself would need twice
+// the exponent range that e4m3 has.
+//
+// The codes are rounded at random.  With b2 = 0.999 v moves by a tenth of a
+// percent a step and codes are 6 to 12 % apart: rounding to nearest would leave
+// nearly every code where it is, up to a hundredfold below g^2.  m goes up
+// with the probability of its fraction, which keeps its mean.  r goes up with the
+// probability (v - lo^2) / (hi^2 - lo^2), which keeps the mean of v: the fraction of
+// r would add the variance of each rounding to v, step after step.  Scales
+// are powers of two because then a value that has not changed is a code still
+// when the scale changes: only the change itself is rounded.
+
+// E of the scale: 448 = 1.75 * 2^8, so the exponent of the largest magnitude
+// less 8, and one more where its significand exceeds 1.75.
+__device__ __forceinline__ int scale_byte(uint32_t largest_bits) {
+  return max((int)((largest_bits + 0x1FFFFFu) >> 23) - 8, 1);
+}
+// 2^(E - 127), zero for the byte 0 of a fresh state
+__device__ __forceinline__ float scale_of(int e) { return __uint_as_float((uint32_t)e << 23); }
+// its reciprocal 2^(127 - E)
+__device__ __forceinline__ float inverse_scale(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
 
 // The codes are 2^-9 apart below 2^-6, throughout, as they are in [2^-6, 2^-5): values
 // there are lifted by 2^-6 for the rounding (LIFT: some value of the block lies below,
@@ -558,6 +623,7 @@ __device__ __forceinline__ uint32_t bf16_pair(F2 a) {
 // the pointers are aligned to four elements; lane l holds elements 4l..4l+3 of
 // either half.  Otherwise element 32 q + l is lane l's q-th, so that accesses of single elements
 // are those of neighbouring lanes to neighbouring addresses.
+
 // em, er: the scales' bytes, which come back as the new ones.
 template <bool BF16, bool WHOLE>
 __device__ __forceinline__ void step_block(const Update& u, int o, const AdamwState& st, const Hyper& h, int& em,
@@ -572,14 +638,13 @@ __device__ __forceinline__ void step_block(const Update& u, int o, const AdamwSt
   if (WHOLE) {
     uint32_t cm[2], cr[2];
     uint2 cg[2];
-    const char* gp = static_cast<const char*>(u.g) + (u.c.start + o) * (BF16 ? 2 : 4);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int i = 128 * k + 4 * lane;
       cm[k] = ld4(mq + i);
       cr[k] = ld4(rq + i);
-      if (BF16) cg[k] = ld8(gp + 2 * i);
-      else ld16(gp + 4 * i, g[2 * k], g[2 * k + 1]);
+      if (BF16) cg[k] = ld8(u.g + 2 * (o + i));
+      else ld16(u.g + 4 * (o + i), g[2 * k], g[2 * k + 1]);
       ld16(wp + i, w[2 * k], w[2 * k + 1]);
     }
 #pragma unroll
@@ -597,7 +662,7 @@ __device__ __forceinline__ void step_block(const Update& u, int o, const AdamwSt
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       xw[q] = in(q) ? wp[at(q)] : 0.0f;
-      xg[q] = in(q) ? load1<BF16>(u.g, u.c.start + o + at(q)) : 0.0f;
+      xg[q] = in(q) ? load1<BF16>(u.g, o + at(q)) : 0.0f;
       cm[q] = mq[at(q)];
       cr[q] = rq[at(q)];
     }
@@ -623,16 +688,16 @@ __device__ __forceinline__ void step_block(const Update& u, int o, const AdamwSt
   float mm = 0.0f, vm = 0.0f, ml = FLT_MAX, rl = FLT_MAX;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    m[k] = m[k] * b1ms + f2(h.omb1) * g[k];
+    m[k] = m[k] * b1ms + f2(h.omb1_2) * g[k];
     r[k] = r[k] * rs;
-    const F2 v = f2(h.beta2) * (r[k] * r[k]) + f2(h.omb2) * g[k] * g[k];
+    const F2 v = f2(h.beta2_2) * (r[k] * r[k]) + f2(h.omb2_2) * g[k] * g[k];
     mm = largest(mm, m[k]);
     vm = largest(vm, v);
     const float2 x = un2(v);
     r[k] = f2(sqrtf(x.x), sqrtf(x.y));
     ml = smallest(ml, m[k]);
     rl = smallest(rl, r[k]);
-    const float2 d = un2(fma2(r[k], f2(u.s.second), f2(h.eps)));
+    const float2 d = un2(fma2(r[k], f2(u.s.second), f2(h.eps_2)));
     w[k] = fma2(w[k], f2(u.s.shrink), m[k] * f2(reciprocal(d.x), reciprocal(d.y)) * f2(-u.s.first));
   }
   if (WHOLE) {
@@ -678,27 +743,30 @@ __device__ __forceinline__ void step_block(const Update& u, int o, const AdamwSt
   }
 }
 
+// Four CTAs an SM: three whose warps load their next block ahead took 932 us in place of 901 us
+// for 285M parameters.
 template <bool BF16, int K>
 __global__ void __launch_bounds__(kThreads, 4) adamw_8bit_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
                                                                  const __grid_constant__ Pointers<K> gp,
                                                                  const __grid_constant__ Pointers<K> cp, int copies,
                                                                  int p0, int c0, AdamwState st,
-                                                                 const ListStep* __restrict__ step, Hyper h) {
-  Update u;
-  if (!update_of(u, t, wp, gp, cp, copies, p0, c0, step)) return;
-  const bool aligned = aligned4<false>(u.w) && aligned4<BF16>(u.g) && aligned4<true>(u.b);
+                                                                 const ListStep* step, Hyper h) {
   // A chunk's scales are read and written together, 32 neighbouring bytes each, which for a
   // chunk inside a tensor are one sector.  Written by one block's warp at a time, byte by byte
   // among the others' reads of the same sector, they took half of the step: 2116 us in place of 975 us.
   constexpr int kBlocks = kListChunk / kQBlock;
   __shared__ uint8_t scales[2][kBlocks];
+  Update u;
+  update_of<BF16>(u, t, wp, gp, cp, copies, p0, c0);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t blk = u.c.flat / kQBlock;
   const int blocks = (u.c.len + kQBlock - 1) / kQBlock;
   const int ms = lane < blocks ? st.ms[blk + lane] : 0, rs = lane < blocks ? st.rs[blk + lane] : 0;
+  const int whole = u.aligned ? u.c.len / kQBlock : 0;
+  if (!pass_results(u, t, step)) return;
   for (int i = warp; i < blocks; i += kListWarps) {
     int em = __shfl_sync(0xffffffffu, ms, i), er = __shfl_sync(0xffffffffu, rs, i);
-    if (aligned && (i + 1) * kQBlock <= u.c.len) step_block<BF16, true>(u, i * kQBlock, st, h, em, er);
+    if (i < whole) step_block<BF16, true>(u, i * kQBlock, st, h, em, er);
     else step_block<BF16, false>(u, i * kQBlock, st, h, em, er);
     if (lane == 0) {
       scales[0][i] = (uint8_t)em;
@@ -707,6 +775,162 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_8bit_kernel(ListTables t, c
   }
   __syncthreads();
   if (warp < 2 && lane < blocks) (warp ? st.rs : st.ms)[blk + lane] = scales[warp][lane];
+}
+
+// ---------------- small lists ----------------
+//
+// A list of at most kSmallBlocks blocks is done by one launch of one cluster, a
+// warp a block: the CTAs exchange their sums through each other's shared memory.  The
+// two launches take 8 to 10 us for a 64 x 32 tensor, most of it in starting and ending.
+
+enum : int { kOpNorm, kOpClip, kOpF32, kOp8Bit };
+constexpr int kSmallWarps = 16;
+
+// Sum of squares of one block, eight elements a lane, and whether one is not finite.
+template <bool BF16>
+__device__ __forceinline__ double block_squares(const char* g, int len, bool& bad) {
+  const int lane = threadIdx.x & 31;
+  float x[8];
+  if (len == kQBlock && aligned4<BF16>(g)) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) load4<BF16>(g, 128 * k + 4 * lane, *reinterpret_cast<float(*)[4]>(x + 4 * k));
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[q] = 32 * q + lane < len ? load1<BF16>(g, 32 * q + lane) : 0.0f;
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) s = fmaf(x[q], x[q], s);
+  double sum = (double)s;
+  bad = false;
+  if (!(s <= FLT_MAX && s >= 0x1p-96f)) {
+    sum = 0.0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      bad |= !isfinite(x[q]);
+      sum += (double)x[q] * x[q];
+    }
+  }
+  bad = __any_sync(0xffffffffu, bad);
+  return warp_sum(sum);
+}
+
+// The sum over all CTAs of a value of each warp, and whether one of them is bad.
+__device__ __forceinline__ double cluster_total(double warp_value, bool warp_bad, bool& bad, double* mine, int* mine_bad,
+                                                double* all, int* all_bad) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+    mine[warp] = warp_value;
+    mine_bad[warp] = warp_bad;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const double s = warp_sum(lane < kSmallWarps ? mine[lane] : 0.0);
+    const bool b = __any_sync(0xffffffffu, lane < kSmallWarps && mine_bad[lane]);
+    if (lane < (int)gridDim.x) {
+      cluster.map_shared_rank(all, lane)[blockIdx.x] = s;
+      cluster.map_shared_rank(all_bad, lane)[blockIdx.x] = b;
+    }
+  }
+  cluster.sync();
+  double total = 0.0;
+  bad = false;
+  for (int i = 0; i < (int)gridDim.x; ++i) {
+    total += all[i];
+    bad |= all_bad[i] != 0;
+  }
+  return total;
+}
+
+template <int OP, bool BF16, int K>
+__global__ void __launch_bounds__(32 * kSmallWarps)
+    list_small_kernel(ListTables t, const __grid_constant__ Pointers<K> wp, const __grid_constant__ Pointers<K> gp,
+                      const __grid_constant__ Pointers<K> cp, int copies, double max_norm, ListAdvance adv, AdamwState st,
+                      Hyper h) {
+  __shared__ double sums[kSmallWarps], all[2][kSmallCtas];
+  __shared__ int bads[kSmallWarps], all_bad[2][kSmallCtas], skipped;
+  const int lane = threadIdx.x & 31, warps = gridDim.x * kSmallWarps;
+  const int b0 = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
+  const unsigned pass = __ldcg(&t.result->pass);
+  const auto gradient = [&](const ListChunk& c) {
+    return static_cast<const char*>(gp.p[c.param]) + c.start * (BF16 ? 2 : 4);
+  };
+  if (threadIdx.x == 0) skipped = 0;
+  double sum = 0.0;
+  bool bad = false;
+  for (int b = b0; b < t.nblocks; b += warps) {
+    const ListChunk c = t.blocks[b];
+    bool one;
+    sum += block_squares<BF16>(gradient(c), c.len, one);
+    if (one && lane == 0) t.mark[c.param] = pass;
+    bad |= one;
+  }
+  if (OP == kOpF32 || OP == kOp8Bit)
+    // from the last warps on, which have the fewest blocks
+    for (int p = 32 * warps - 1 - (blockIdx.x * 32 * kSmallWarps + threadIdx.x); p < t.nparams; p += 32 * warps)
+      step_factors(adv, p);
+  sum = cluster_total(sum, bad, bad, sums, bads, all[0], all_bad[0]);
+  if (bad) {   // once more without the tensors that are skipped: all CTAs come here
+    sum = 0.0;
+    for (int b = b0; b < t.nblocks; b += warps) {
+      const ListChunk c = t.blocks[b];
+      bool one;
+      const double s = block_squares<BF16>(gradient(c), c.len, one);
+      if (__ldcg(&t.mark[c.param]) != pass) sum += s;
+    }
+    bool unused;
+    sum = cluster_total(sum, false, unused, sums, bads, all[1], all_bad[1]);
+  }
+  const double norm = sqrt(sum);
+  const float coef = max_norm > 0.0 && norm > max_norm ? (float)(max_norm / norm) : 1.0f;
+  if (OP != kOpNorm && (OP != kOpClip || coef != 1.0f)) {
+    for (int b = b0; b < t.nblocks; b += warps) {
+      Update u;
+      u.c = t.blocks[b];
+      if (__ldcg(&t.mark[u.c.param]) == pass) continue;
+      u.g = gradient(u.c);
+      if (OP == kOpClip) {
+        void* g = const_cast<char*>(u.g);
+        for (int i = lane; i < u.c.len; i += 32) store1<BF16>(g, i, load1<BF16>(g, i) * coef);
+        continue;
+      }
+      u.w = static_cast<float*>(const_cast<void*>(wp.p[u.c.param])) + u.c.start;
+      u.b = copies ? static_cast<uint16_t*>(const_cast<void*>(cp.p[u.c.param])) + u.c.start : nullptr;
+      u.aligned = aligned4<false>(u.w) && aligned4<BF16>(u.g) && aligned4<true>(u.b);
+      const float4 f = __ldcg(reinterpret_cast<const float4*>(adv.out + u.c.param));
+      u.s = ListStep{f.x, f.y, f.z, __float_as_uint(f.w)};
+      u.coef = coef;
+      u.huge = !(norm * coef < (double)kGradMax);
+      if (OP == kOpF32) {
+        step_run<BF16>(u, st.m + u.c.flat, st.v + u.c.flat, lane, 32, h, [] { return true; });
+      } else {
+        const int64_t blk = u.c.flat / kQBlock;
+        int em = st.ms[blk], er = st.rs[blk];
+        if (u.aligned && u.c.len == kQBlock) step_block<BF16, true>(u, 0, st, h, em, er);
+        else step_block<BF16, false>(u, 0, st, h, em, er);
+        if (lane == 0) {
+          st.ms[blk] = (uint8_t)em;
+          st.rs[blk] = (uint8_t)er;
+        }
+      }
+    }
+  }
+  if (blockIdx.x != 0) return;
+  for (int p = threadIdx.x; p < t.nparams; p += 32 * kSmallWarps) {
+    const int sk = __ldcg(&t.mark[p]) == pass;
+    t.skip[p] = sk;
+    if (sk) atomicAdd(&skipped, 1);
+    else if (OP == kOpF32 || OP == kOp8Bit) adv.step[p] += 1;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    t.result->norm = (float)norm;
+    t.result->coef = coef;
+    t.result->skipped = skipped;
+    t.result->pass = pass + 1;
+  }
 }
 
 template <int K>
@@ -720,10 +944,24 @@ Pointers<K> pack(const void* const* p, int n) {
 // a launch more than 768 bytes do.
 template <class F>
 cudaError_t by_count(int n, F&& f) {
-  if (n <= 32) f(std::integral_constant<int, 32>());
-  else if (n <= 256) f(std::integral_constant<int, 256>());
-  else f(std::integral_constant<int, kListGroup>());
-  return cudaGetLastError();
+  if (n <= 32) return f(std::integral_constant<int, 32>());
+  if (n <= 256) return f(std::integral_constant<int, 256>());
+  return f(std::integral_constant<int, kListGroup>());
+}
+
+// Launches a kernel that may start before the one in front of it ends.
+template <class... P, class... A>
+cudaError_t launch_early(void (*kernel)(P...), int ctas, cudaStream_t s, const A&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
 }  // namespace
@@ -742,7 +980,59 @@ cudaError_t launch_list_norm(const ListTables& t, const void* const* g, int p0, 
     const int ctas = list_norm_ctas(nc);
     if (bf16) list_norm_kernel<true, K><<<ctas, kThreads, 0, s>>>(t, a, p0, np, c0, nc, b0, max_norm, adv);
     else list_norm_kernel<false, K><<<ctas, kThreads, 0, s>>>(t, a, p0, np, c0, nc, b0, max_norm, adv);
+    return cudaGetLastError();
   });
+}
+
+int list_small_ctas(int nblocks) {
+  int n = 1;
+  while (n < kSmallCtas && n * kSmallWarps < nblocks) n *= 2;
+  return n;
+}
+
+namespace {
+
+// One cluster is the whole grid.
+template <int OP, bool BF16>
+cudaError_t launch_small(const ListTables& t, const void* const* w, const void* const* g, const void* const* copies,
+                         double max_norm, const ListAdvance& adv, const AdamwState& st, const Hyper& h, cudaStream_t s) {
+  return by_count(t.nparams, [&](auto n) {
+    constexpr int K = decltype(n)::value;
+    const Pointers<K> aw = w ? pack<K>(w, t.nparams) : Pointers<K>{};
+    const Pointers<K> ag = pack<K>(g, t.nparams);
+    const Pointers<K> ac = copies ? pack<K>(copies, t.nparams) : Pointers<K>{};
+    const int ctas = list_small_ctas(t.nblocks);
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(32 * kSmallWarps);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, list_small_kernel<OP, BF16, K>, t, aw, ag, ac, (int)(copies != nullptr), max_norm, adv,
+                              st, h);
+  });
+}
+
+}  // namespace
+
+cudaError_t launch_list_small(const ListTables& t, const void* const* g, int bf16, int clip, double max_norm,
+                              cudaStream_t s) {
+  auto* f = clip ? (bf16 ? launch_small<kOpClip, true> : launch_small<kOpClip, false>)
+                 : (bf16 ? launch_small<kOpNorm, true> : launch_small<kOpNorm, false>);
+  return f(t, nullptr, g, nullptr, max_norm, ListAdvance{}, AdamwState{}, Hyper{}, s);
+}
+
+cudaError_t launch_adamw_small(const ListTables& t, float* const* w, const void* const* g, void* const* copies, int bf16,
+                               int eight, double max_norm, const ListAdvance& adv, const AdamwState& st, float beta1,
+                               float omb1, float beta2, float omb2, float eps, cudaStream_t s) {
+  auto* f = eight ? (bf16 ? launch_small<kOp8Bit, true> : launch_small<kOp8Bit, false>)
+                  : (bf16 ? launch_small<kOpF32, true> : launch_small<kOpF32, false>);
+  return f(t, reinterpret_cast<const void* const*>(w), g, const_cast<const void* const*>(copies), max_norm, adv, st,
+           hyper(beta1, omb1, beta2, omb2, eps), s);
 }
 
 cudaError_t launch_list_scale(const ListTables& t, void* const* g, int p0, int np, int c0, int nc, int bf16,
@@ -750,29 +1040,23 @@ cudaError_t launch_list_scale(const ListTables& t, void* const* g, int p0, int n
   return by_count(np, [&](auto n) {
     constexpr int K = decltype(n)::value;
     const Pointers<K> a = pack<K>(const_cast<const void* const*>(g) + p0, np);
-    if (bf16) list_scale_kernel<true, K><<<nc, kThreads, 0, s>>>(t, a, p0, c0);
-    else list_scale_kernel<false, K><<<nc, kThreads, 0, s>>>(t, a, p0, c0);
+    return launch_early(bf16 ? list_scale_kernel<true, K> : list_scale_kernel<false, K>, nc, s, t, a, p0, c0);
   });
 }
 
 cudaError_t launch_adamw(const ListTables& t, float* const* w, const void* const* g, void* const* copies, int p0,
                          int np, int c0, int nc, int bf16, int eight, const AdamwState& st, const ListStep* step,
                          float beta1, float omb1, float beta2, float omb2, float eps, cudaStream_t s) {
-  const Hyper h{beta1, omb1, beta2, omb2, eps};
+  const Hyper h = hyper(beta1, omb1, beta2, omb2, eps);
   return by_count(np, [&](auto n) {
     constexpr int K = decltype(n)::value;
     const Pointers<K> aw = pack<K>(reinterpret_cast<const void* const*>(w) + p0, np);
     const Pointers<K> ag = pack<K>(g + p0, np);
     const Pointers<K> ac = copies ? pack<K>(const_cast<const void* const*>(copies) + p0, np) : Pointers<K>{};
     const int cc = copies != nullptr;
-    if (eight && bf16)
-      adamw_8bit_kernel<true, K><<<nc, kThreads, 0, s>>>(t, aw, ag, ac, cc, p0, c0, st, step, h);
-    else if (eight)
-      adamw_8bit_kernel<false, K><<<nc, kThreads, 0, s>>>(t, aw, ag, ac, cc, p0, c0, st, step, h);
-    else if (bf16)
-      adamw_f32_kernel<true, K><<<nc, kThreads, 0, s>>>(t, aw, ag, ac, cc, p0, c0, st, step, h);
-    else
-      adamw_f32_kernel<false, K><<<nc, kThreads, 0, s>>>(t, aw, ag, ac, cc, p0, c0, st, step, h);
+    auto* kernel = eight ? (bf16 ? adamw_8bit_kernel<true, K> : adamw_8bit_kernel<false, K>)
+                         : (bf16 ? adamw_f32_kernel<true, K> : adamw_f32_kernel<false, K>);
+    return launch_early(kernel, nc, s, t, aw, ag, ac, cc, p0, c0, st, step, h);
   });
 }
 

@@ -105,7 +105,7 @@ shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dt
   cudaError_t e = cudaGetDevice(&l->device);
   if (e != cudaSuccess) return cuda_error(l, e, "cudaGetDevice");
   l->numel.assign(numel, numel + nparams);
-  std::vector<ListChunk> chunks;
+  std::vector<ListChunk> chunks, blocks;
   for (int i = 0; i < nparams; ++i) {
     if (i % kListGroup == 0) l->groups.push_back(Group{i, 0, (int)chunks.size(), 0, 0});
     l->offset.push_back(l->total);
@@ -123,23 +123,33 @@ shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dt
     g.np = i + 1 - g.p0;
     g.nc = (int)chunks.size() - g.c0;
   }
+  if (l->total <= (int64_t)kSmallBlocks * kQBlock) {
+    for (int i = 0; i < nparams; ++i)
+      for (int64_t s = 0; s < numel[i]; s += kQBlock)
+        blocks.push_back(ListChunk{i, (int)std::min<int64_t>(kQBlock, numel[i] - s), s, l->offset[i] + s});
+    l->tab.nblocks = (int)blocks.size();
+  }
   l->tab.nchunks = (int)chunks.size();
   l->tab.nparams = nparams;
-  ListChunk* d = nullptr;
+  ListChunk *d = nullptr, *db = nullptr;
   for (Group& g : l->groups) {
     g.b0 = l->tab.nctas;
     l->tab.nctas += list_norm_ctas(g.nc);
   }
-  if ((e = zeroed(l, &d, l->tab.nchunks)) != cudaSuccess || (e = zeroed(l, &l->tab.partial, (int64_t)l->tab.nchunks * kListWarps)) != cudaSuccess ||
+  if ((e = zeroed(l, &d, l->tab.nchunks)) != cudaSuccess ||
+      (!blocks.empty() && (e = zeroed(l, &db, l->tab.nblocks)) != cudaSuccess) || (e = zeroed(l, &l->tab.partial, l->tab.nchunks)) != cudaSuccess ||
       (e = zeroed(l, &l->tab.csum, l->tab.nctas)) != cudaSuccess ||
       (e = zeroed(l, &l->tab.mark, nparams)) != cudaSuccess || (e = zeroed(l, &l->tab.skip, nparams)) != cudaSuccess || (e = zeroed(l, &l->tab.result, 1)) != cudaSuccess)
     return refuse(l, SHAMPOO_ENOMEM, std::string("device allocation failed: ") + cudaGetErrorString(e));
   l->tab.chunks = d;
+  l->tab.blocks = db;
   // pageable sources: staged by the driver before the calls return
   const ListResult first{0.f, 1.f, 0, 0, 1, 0};
   e = cudaMemcpyAsync(l->tab.result, &first, sizeof(first), cudaMemcpyHostToDevice, l->stream);
   if (e == cudaSuccess)
     e = cudaMemcpyAsync(d, chunks.data(), chunks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
+  if (e == cudaSuccess && db)
+    e = cudaMemcpyAsync(db, blocks.data(), blocks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
   if (e != cudaSuccess) return cuda_error(l, e, "upload of the chunk table");
   return SHAMPOO_OK;
 }
@@ -266,6 +276,10 @@ shampoo_status shampoo_clip_norm(shampoo_clip* clip, const void* const* grads) {
     const shampoo_status st = check_pointers(l, lists, 1);
     if (st != SHAMPOO_OK) return st;
     OnDevice on(l->device);
+    if (l->tab.blocks) {
+      const cudaError_t e = launch_list_small(l->tab, grads, l->bf16, 0, 0.0, l->stream);
+      return e == cudaSuccess ? SHAMPOO_OK : cuda_error(l, e, "list_small");
+    }
     for (const Group& g : l->groups) {
       const cudaError_t e = launch_list_norm(l->tab, grads, g.p0, g.np, g.c0, g.nc, g.b0, l->bf16, 0.0, ListAdvance{}, l->stream);
       if (e != cudaSuccess) return cuda_error(l, e, "list_norm");
@@ -286,6 +300,10 @@ shampoo_status shampoo_clip_apply(shampoo_clip* clip, void* const* grads, double
     if (st != SHAMPOO_OK) return st;
     OnDevice on(l->device);
     cudaError_t e = cudaSuccess;
+    if (l->tab.blocks) {
+      e = launch_list_small(l->tab, g0, l->bf16, 1, max_norm, l->stream);
+      return e == cudaSuccess ? SHAMPOO_OK : cuda_error(l, e, "list_small");
+    }
     for (const Group& g : l->groups)
       if ((e = launch_list_norm(l->tab, g0, g.p0, g.np, g.c0, g.nc, g.b0, l->bf16, max_norm, ListAdvance{}, l->stream)) != cudaSuccess)
         return cuda_error(l, e, "list_norm");
@@ -399,14 +417,19 @@ shampoo_status shampoo_adamw_step(shampoo_adamw* adamw, float* const* params, co
     if (st != SHAMPOO_OK) return st;
     OnDevice on(l->device);
     const ListAdvance adv{a->step, a->factors, a->decay, lr, a->beta1, a->beta2, (uint32_t)a->seed, (uint32_t)(a->seed >> 32)};
+    const float b1 = (float)a->beta1, omb1 = (float)(1.0 - a->beta1), b2 = (float)a->beta2, omb2 = (float)(1.0 - a->beta2);
     cudaError_t e = cudaSuccess;
+    if (l->tab.blocks) {
+      e = launch_adamw_small(l->tab, params, grads, copies, l->bf16, a->bits == 8, a->max_norm, adv, a->st, b1, omb1, b2,
+                             omb2, (float)a->eps, l->stream);
+      return e == cudaSuccess ? SHAMPOO_OK : cuda_error(l, e, "adamw_small");
+    }
     for (const Group& g : l->groups)
       if ((e = launch_list_norm(l->tab, grads, g.p0, g.np, g.c0, g.nc, g.b0, l->bf16, a->max_norm, adv, l->stream)) != cudaSuccess)
         return cuda_error(l, e, "list_norm");
     for (const Group& g : l->groups)
       if ((e = launch_adamw(l->tab, params, grads, copies, g.p0, g.np, g.c0, g.nc, l->bf16, a->bits == 8, a->st, a->factors,
-                            (float)a->beta1, (float)(1.0 - a->beta1), (float)a->beta2, (float)(1.0 - a->beta2), (float)a->eps,
-                            l->stream)) != cudaSuccess)
+                            b1, omb1, b2, omb2, (float)a->eps, l->stream)) != cudaSuccess)
         return cuda_error(l, e, "adamw");
     return SHAMPOO_OK;
   });

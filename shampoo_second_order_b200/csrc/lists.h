@@ -7,6 +7,8 @@
 namespace shampoo {
 
 constexpr int kListChunk = 8192;   // elements per CTA of the list kernels
+constexpr int kSmallBlocks = 512;  // of the lists that one cluster does
+constexpr int kSmallCtas = 8;
 constexpr int kListWarps = 8;      // warps per CTA of the list kernels
 constexpr int kQBlock = 256;       // elements per scale of the 8-bit moments; every
                                    // tensor's state starts at a multiple of it
@@ -31,7 +33,7 @@ struct ListResult {
 };
 
 // Per-tensor factors of one AdamW step.
-struct ListStep {
+struct alignas(16) ListStep {
   float first;      // lr / (1 - b1^t)
   float second;     // 1 / sqrt(1 - b2^t)
   float shrink;     // 1 - lr wd
@@ -50,11 +52,13 @@ struct ListAdvance {
 // The tables of a pass over the gradients.
 struct ListTables {
   const ListChunk* chunks;
-  double* partial;        // [nchunks][kListWarps] sum of squares of each warp's part of a chunk
+  double* partial;        // [nchunks] sums of squares of runs of a tensor's chunks, with the run's last
   double* csum;           // [nctas] and of all that a CTA of the pass has read
   unsigned* mark;         // [n] the last pass that met an element of it that is not finite
   int* skip;              // [n] 1: the tensor's gradient was not finite
   ListResult* result;
+  const ListChunk* blocks;   // of a small list: its blocks of kQBlock elements, else null
+  int nblocks;
   int nchunks, nparams;
   int nctas;              // of the pass, over all its launches
 };
@@ -67,6 +71,13 @@ struct AdamwState {
   float *m, *v;                 // 32-bit moments
   uint8_t *mq, *rq, *ms, *rs;   // 8-bit: codes of m and sqrt(v), scale exponents
 };
+
+// Small lists: the norm or the clipping, and the AdamW step, in one launch.
+cudaError_t launch_list_small(const ListTables& t, const void* const* g, int bf16, int clip, double max_norm,
+                              cudaStream_t s);
+cudaError_t launch_adamw_small(const ListTables& t, float* const* w, const void* const* g, void* const* copies, int bf16,
+                               int eight, double max_norm, const ListAdvance& adv, const AdamwState& st, float beta1,
+                               float omb1, float beta2, float omb2, float eps, cudaStream_t s);
 
 // CTAs of the norm's launch over nc chunks.
 int list_norm_ctas(int nc);

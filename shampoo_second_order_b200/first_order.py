@@ -6,8 +6,16 @@ from __future__ import annotations
 import ctypes as C
 from array import array
 from math import prod
+from operator import attrgetter
+
+import torch
+from torch import Tensor
 
 from . import _lib as L
+
+_dtype = attrgetter("dtype")
+# the handle of a device's current stream, without an object around it
+_current_handle = torch._C._cuda_getCurrentRawStream
 
 
 class _Handle:
@@ -39,7 +47,6 @@ class _List:
     the current stream holds so far, and the current stream waits for it."""
 
     def __init__(self, shapes, grad_dtype, stream):
-        import torch
         if grad_dtype not in ("f32", "bf16"):
             raise ValueError('grad_dtype must be "f32" or "bf16"')
         self.shapes = [tuple(int(d) for d in s) for s in shapes]
@@ -58,41 +65,40 @@ class _List:
 
     def _pointers(self, ts, what, dtype):
         """The C array of a list's device pointers, after its checks."""
-        from torch import Tensor
         ts = list(ts)
         if len(ts) != len(self._numel):
             raise ValueError(f"expected {len(self._numel)} {what}, got {len(ts)}")
         if list(map(Tensor.numel, ts)) != self._numel or not all(map(Tensor.is_contiguous, ts)) \
-                or any(t.dtype is not dtype for t in ts) or set(map(Tensor.get_device, ts)) != {self._device}:
+                or set(map(_dtype, ts)) != {dtype} or set(map(Tensor.get_device, ts)) != {self._device}:
             raise ValueError(f"{what} must be contiguous {dtype} tensors of the given shapes "
                              f"on CUDA device {self._device}")
         return (C.c_void_p * len(ts)).from_buffer(array("Q", map(Tensor.data_ptr, ts)))
 
-    def _on_stream(self, set_stream, call):
-        """Run `call` in the order of the caller's current stream."""
-        import torch
+    def _on_stream(self, set_stream, call, *args):
+        """call(context, *args) in the order of the caller's current stream."""
+        ctx, mine = self._ctx, self.stream.cuda_stream
+        if _current_handle(self._device) == mine:
+            call(ctx, *args)
+            return
         current = torch.cuda.current_stream(self._device)
-        if current.cuda_stream == self.stream.cuda_stream:
-            call()
-        elif not self._follows:
+        if not self._follows:
             self.stream.wait_stream(current)
-            call()
+            call(ctx, *args)
             current.wait_stream(self.stream)
         elif torch.cuda.is_current_stream_capturing():
             # a graph's place among the context's other calls is that of its replays
-            set_stream(self._ctx, current.cuda_stream)
+            set_stream(ctx, current.cuda_stream)
             try:
-                call()
+                call(ctx, *args)
             finally:
-                set_stream(self._ctx, self.stream.cuda_stream)
+                set_stream(ctx, mine)
         else:
             current.wait_stream(self.stream)   # the context's earlier calls
-            set_stream(self._ctx, current.cuda_stream)
+            set_stream(ctx, current.cuda_stream)
             self.stream = current
-            call()
+            call(ctx, *args)
 
     def _view(self, address, count, typestr):
-        import torch
         return torch.as_tensor(_Memory(self._handle, address, count, typestr), device=f"cuda:{self._device}")
 
     @property
@@ -120,15 +126,15 @@ class GradClip(_List):
 
     def norm(self, grads):
         """The global norm, as a 0-d CUDA tensor that the next call overwrites."""
-        ctx, p = self._ctx, self._pointers(grads, "grads", self.grad_dtype)
-        self._on_stream(L.shampoo_clip_set_stream, lambda: L.shampoo_clip_norm(ctx, p))
+        p = self._pointers(grads, "grads", self.grad_dtype)
+        self._on_stream(L.shampoo_clip_set_stream, L.shampoo_clip_norm, p)
         return self._norm
 
     def clip(self, grads, max_norm):
         """Scale the gradients in place to a global norm of at most max_norm.
         Returns the norm they had, as norm() does."""
-        ctx, p = self._ctx, self._pointers(grads, "grads", self.grad_dtype)
-        self._on_stream(L.shampoo_clip_set_stream, lambda: L.shampoo_clip_apply(ctx, p, max_norm))
+        p = self._pointers(grads, "grads", self.grad_dtype)
+        self._on_stream(L.shampoo_clip_set_stream, L.shampoo_clip_apply, p, max_norm)
         return self._norm
 
     def nonfinite_status(self):
@@ -167,7 +173,6 @@ class AdamW(_List):
         return self._view(*L.shampoo_adamw_state(self._ctx, which), typestr)
 
     def _views(self):
-        import torch
         step = self._part(L.ADAMW_STEP, "<i4")
         if self.state == "f32":
             return {"step": step, "m": self._part(L.ADAMW_M, "<f4"), "v": self._part(L.ADAMW_V, "<f4")}
@@ -188,12 +193,10 @@ class AdamW(_List):
 
     def step(self, params, grads, lr, copies=None):
         """One step.  copies: bfloat16 tensors that receive the updated parameters."""
-        import torch
-        ctx = self._ctx
         w = self._pointers(params, "params", torch.float32)
         g = self._pointers(grads, "grads", self.grad_dtype)
         b = None if copies is None else self._pointers(copies, "copies", torch.bfloat16)
-        self._on_stream(L.shampoo_adamw_set_stream, lambda: L.shampoo_adamw_step(ctx, w, g, b, lr))
+        self._on_stream(L.shampoo_adamw_set_stream, L.shampoo_adamw_step, w, g, b, lr)
 
     def grad_norm(self):
         """The gradient norm of the last step before clipping, as a 0-d CUDA tensor

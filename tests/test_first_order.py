@@ -321,7 +321,9 @@ SETS = {
     "chunk edges": [8191, 8192, 8193, 16384 + 255],
     "mixed": [200 * 130, 64 * 64, 19 * 200, 130, 64, 77],
     "layer": [512 * 512, 512 * 1024, 512],
+    "large edges": [8191, 8192, 8193, 1, 16384 + 255, 131072, 255, 50003],
 }
+# lists of up to 131072 elements take one launch, larger ones two: `more` brings a list over
 
 
 @gpu
@@ -361,44 +363,48 @@ def test_adamw_many_tensors(cuda, state):
 
 
 @gpu
+@pytest.mark.parametrize("more", [[], [150000]])
 @pytest.mark.parametrize("state", ["f32", "8bit"])
 @pytest.mark.parametrize("gdt", ["f32", "bf16"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
-def test_adamw_skips_gradients_that_are_not_finite(cuda, state, gdt, value):
+def test_adamw_skips_gradients_that_are_not_finite(cuda, state, gdt, value, more):
     """At the first, the last and an inner element; then all of them; then none again: step counts differ from then on."""
     from shampoo_second_order_b200 import AdamW
-    sizes = [9000, 300, 17, 8192]
+    sizes = [9000, 300, 17, 8192] + more
+    n = len(sizes)
     P = Params(sizes, gdt, seed=4)
     opt = AdamW([(k,) for k in sizes], B1, B2, EPS, 0.01, state, gdt, 1e-3, seed=1)
-    check_step(opt, P, 1e-3, [0.01] * 4, 1e-3, 1, True)
+    check_step(opt, P, 1e-3, [0.01] * n, 1e-3, 1, True)
     for where in ((0, 0), (0, 8999), (1, 299), (2, 5), (3, 8191)):
         P.new_grads()
         P.g[where[0]][where[1]] = value
-        check_step(opt, P, 1e-3, [0.01] * 4, 1e-3, 1, True)
+        check_step(opt, P, 1e-3, [0.01] * n, 1e-3, 1, True)
     for g in P.g:
         g[3] = value
-    check_step(opt, P, 1e-3, [0.01] * 4, 1e-3, 1, True)
-    assert opt.nonfinite_status() == 4 and float(opt.grad_norm()) == 0.0
+    check_step(opt, P, 1e-3, [0.01] * n, 1e-3, 1, True)
+    assert opt.nonfinite_status() == n and float(opt.grad_norm()) == 0.0
     P.new_grads()
-    check_step(opt, P, 1e-3, [0.01] * 4, 1e-3, 1, True)
-    assert opt.state_tensors()["step"].tolist() == [5, 6, 6, 6]
+    check_step(opt, P, 1e-3, [0.01] * n, 1e-3, 1, True)
+    assert opt.state_tensors()["step"].tolist() == [5, 6, 6, 6] + [7] * len(more)
 
 
 @gpu
+@pytest.mark.parametrize("more", [[], [200000]])
 @pytest.mark.parametrize("state", ["f32", "8bit"])
-def test_adamw_extreme_gradients(cuda, state):
+def test_adamw_extreme_gradients(cuda, state, more):
     """Squares beyond and below the range of a float, zeros, and the largest float: finite results, a norm, and beyond
     2^63 the step of a gradient of 2^63."""
     from shampoo_second_order_b200 import AdamW
     for value in (1e25, 3.4028234663852886e38, 1e-25, 1e-38, 0.0):
-        P = Params([1000, 300], "f32", seed=6)
+        sizes = [1000, 300] + more
+        P = Params(sizes, "f32", seed=6)
         for g in P.g:
             g.copy_(torch.sign(g) * value)
-        opt = AdamW([(1000,), (300,)], B1, B2, EPS, 0.0, state, "f32")
+        opt = AdamW([(k,) for k in sizes], B1, B2, EPS, 0.0, state, "f32")
         w0 = [f64(w) for w in P.w]
         for t in range(3):
             opt.step(P.w, P.g, 1e-2)
-            norm = value * math.sqrt(1300)
+            norm = value * math.sqrt(sum(sizes))
             assert float(opt.grad_norm()) == pytest.approx(norm if norm < FLT_MAX else math.inf, rel=1e-6)
         for i, w in enumerate(P.w):
             assert np.isfinite(f64(w)).all() and np.isfinite(moments(opt, i)[0]).all() and np.isfinite(moments(opt, i)[1]).all()
@@ -470,9 +476,10 @@ def test_clip_matches_the_oracle(cuda, gdt, name, shift):
 
 
 @gpu
-def test_clip_leaves_out_what_is_not_finite(cuda):
+@pytest.mark.parametrize("more", [0, 150000])
+def test_clip_leaves_out_what_is_not_finite(cuda, more):
     from shampoo_second_order_b200 import GradClip
-    sizes = [10000, 77, 256]
+    sizes = [10000 + more, 77, 256]
     P = Params(sizes, "f32", seed=22)
     P.g[1][76] = float("inf")
     g0 = [f64(g) for g in P.g]
@@ -500,14 +507,15 @@ def test_same_inputs_give_the_same_bits(cuda, state):
 
 
 @gpu
+@pytest.mark.parametrize("more", [[], [150000]])
 @pytest.mark.parametrize("own_stream", [False, True])
 @pytest.mark.parametrize("state", ["f32", "8bit"])
-def test_adamw_in_a_graph_and_on_other_streams(cuda, state, own_stream):
+def test_adamw_in_a_graph_and_on_other_streams(cuda, state, own_stream, more):
     """A captured step replayed, eager steps between the replays with other tensors, a second graph of the same
     context, and steps from other streams, with and without a stream of the context's own: all give what eager
     steps on one stream give."""
     from shampoo_second_order_b200 import AdamW
-    sizes = [5000, 256, 3]
+    sizes = [5000, 256, 3] + more
     make = lambda: (Params(sizes, "bf16", seed=41), Params(sizes, "bf16", seed=42),   # noqa: E731
                     AdamW([(k,) for k in sizes], state=state, grad_dtype="bf16", max_norm=1e-2, seed=6))
     P, Q, ref = make()
