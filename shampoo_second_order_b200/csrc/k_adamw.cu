@@ -9,6 +9,7 @@
 // All of it is bound by HBM: a few operations an element against 10 to 34 bytes.
 #include <float.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include <cooperative_groups.h>
@@ -359,11 +360,18 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 
 struct Hyper {
   float beta1, omb1, beta2, omb2, eps;
-  float2 omb1_2, beta2_2, omb2_2, eps_2;   // twice each, as the packed instructions read them
+  float2 omb1_2, nbeta2_2, nomb2_2, eps_2;   // twice each, as the packed instructions read them; -beta2, -omb2
 };
 __host__ Hyper hyper(float beta1, float omb1, float beta2, float omb2, float eps) {
-  return Hyper{beta1, omb1, beta2, omb2, eps, {omb1, omb1}, {beta2, beta2}, {omb2, omb2}, {eps, eps}};
+  return Hyper{beta1, omb1, beta2, omb2, eps, {omb1, omb1}, {-beta2, -beta2}, {-omb2, -omb2}, {eps, eps}};
 }
+
+// What the gradient pass leaves for a tensor.
+struct Factors {
+  ListStep s;
+  float coef;
+  bool huge;        // a gradient element may have a square beyond the largest float
+};
 
 // What a CTA of the update needs to know of its chunk.
 struct Update {
@@ -372,10 +380,7 @@ struct Update {
   const char* g;
   uint16_t* b;     // the bfloat16 copy, or null
   bool aligned;    // all three to four elements
-  // what the gradient pass leaves
-  ListStep s;
-  float coef;
-  bool huge;       // a gradient element may have a square beyond the largest float
+  Factors f;
 };
 
 // The chunks in the reverse of the norm's order: the gradients that it read last
@@ -394,9 +399,9 @@ __device__ __forceinline__ void update_of(Update& u, const ListTables& t, const 
 __device__ __forceinline__ bool pass_results(Update& u, const ListTables& t, const ListStep* step) {
   wait_for_previous();
   const int skip = t.skip[u.c.param];
-  u.s = step[u.c.param];
-  u.coef = t.result->coef;
-  u.huge = !(t.result->norm * u.coef < kGradMax);   // no element exceeds the norm
+  u.f.s = step[u.c.param];
+  u.f.coef = t.result->coef;
+  u.f.huge = !(t.result->norm * u.f.coef < kGradMax);   // no element exceeds the norm
   return !skip;
 }
 
@@ -436,11 +441,11 @@ struct Four {
   __device__ __forceinline__ void step(const Update& u, float* mp, float* vp, int i, const Hyper& h) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      g[q] = __fmul_rn(g[q], u.coef);
-      if (u.huge) g[q] = limit(g[q]);
+      g[q] = __fmul_rn(g[q], u.f.coef);
+      if (u.f.huge) g[q] = limit(g[q]);
       m[q] = next_m(__fmul_rn(h.beta1, m[q]), g[q], h);
       v[q] = next_v(__fmul_rn(h.beta2, v[q]), g[q], h);
-      w[q] = next_w(w[q], m[q], sqrtf(v[q]), u.s, h);
+      w[q] = next_w(w[q], m[q], sqrtf(v[q]), u.f.s, h);
     }
     store4<false>(u.w, i, w);
     store4<false>(mp, i, m);
@@ -471,11 +476,11 @@ __device__ __forceinline__ void step_run(Update& u, float* mp, float* vp, int th
   }
 #pragma unroll 4
   for (int i = whole + thread; i < u.c.len; i += threads) {
-    float g = __fmul_rn(load1<BF16>(u.g, i), u.coef);
-    if (u.huge) g = limit(g);
+    float g = __fmul_rn(load1<BF16>(u.g, i), u.f.coef);
+    if (u.f.huge) g = limit(g);
     const float m = next_m(__fmul_rn(h.beta1, mp[i]), g, h);
     const float v = next_v(__fmul_rn(h.beta2, vp[i]), g, h);
-    const float w = next_w(u.w[i], m, sqrtf(v), u.s, h);
+    const float w = next_w(u.w[i], m, sqrtf(v), u.f.s, h);
     u.w[i] = w;
     mp[i] = m;
     vp[i] = v;
@@ -515,61 +520,65 @@ __global__ void __launch_bounds__(kThreads) adamw_f32_kernel(ListTables t, const
 __device__ __forceinline__ int scale_byte(uint32_t largest_bits) {
   return max((int)((largest_bits + 0x1FFFFFu) >> 23) - 8, 1);
 }
+// The same for sqrt(v) from v's bits, exactly: a root exceeds 1.75 2^k where v exceeds
+// 3.0625 2^2k, a significand of 1.53125 after an odd exponent.  Subnormal v, and zero: by
+// the root itself.
+__device__ __forceinline__ int root_scale_byte(uint32_t largest_bits) {
+  if (largest_bits < 0x800000u) return scale_byte(__float_as_uint(sqrtf(__uint_as_float(largest_bits))));
+  return (int)((((largest_bits + 0x3BFFFFu) >> 23) + 1) >> 1) + 55;
+}
 // 2^(E - 127), zero for the byte 0 of a fresh state
 __device__ __forceinline__ float scale_of(int e) { return __uint_as_float((uint32_t)e << 23); }
 // its reciprocal 2^(127 - E)
 __device__ __forceinline__ float inverse_scale(int e) { return __uint_as_float((uint32_t)(254 - e) << 23); }
 
 // The codes are 2^-9 apart below 2^-6, throughout, as they are in [2^-6, 2^-5): values
-// there are lifted by 2^-6 for the rounding (LIFT: some value of the block lies below,
+// there are lifted by 2^-6 for the rounding (LIFT: some value of the block lies there
 // and is not zero).  1 where a < 2^-6, else 0: 2^30 (2^-6 - a), which is 1 or
 // more for the next float below 2^-6, cut to [0, 1].
-template <bool LIFT>
-__device__ __forceinline__ float below(float a) {
-  return LIFT ? __saturatef(fmaf(a, -0x1p30f, 0x1p24f)) : 0.0f;
-}
-template <bool LIFT>
-__device__ __forceinline__ float lifted(float a, float s, float by) {
-  return LIFT ? fmaf(s, by, a) : a;
-}
+__device__ __forceinline__ float below(float a) { return __saturatef(fmaf(a, -0x1p30f, 0x1p24f)); }
 
-// a in [0, 448] to a value of e4m3, up where the 16 random bits and the 20 bits
-// that are cut off carry.
+// a, |a| <= 448, to a value of e4m3, away from zero where the 16 random bits and the 20
+// bits that are cut off carry.
 template <bool LIFT>
 __device__ __forceinline__ float round_m(float a, uint32_t bits) {
-  const float s = below<LIFT>(a);
-  const uint32_t word = __float_as_uint(lifted<LIFT>(a, s, 0x1p-6f));
-  return lifted<LIFT>(__uint_as_float((word + bits * 16) & 0xFFF00000u), s, -0x1p-6f);
+  if (!LIFT) return __uint_as_float((__float_as_uint(a) + bits * 16) & 0xFFF00000u);
+  const float s = below(fabsf(a));
+  const uint32_t word = __float_as_uint(fmaf(s, 0x1p-6f, fabsf(a)));
+  return copysignf(fmaf(s, -0x1p-6f, __uint_as_float((word + bits * 16) & 0xFFF00000u)), a);
 }
-// The same, up where (a^2 - lo^2) > bits / 2^16 (hi^2 - lo^2).
+// The same for a >= 0, up where (a^2 - lo^2) > bits / 2^16 (hi^2 - lo^2).
 template <bool LIFT>
-__device__ __forceinline__ F2 round_r(F2 a2, uint32_t bits0, uint32_t bits1) {
-  const float2 a = un2(a2);
-  const float s0 = below<LIFT>(a.x), s1 = below<LIFT>(a.y);
-  const uint32_t w0 = __float_as_uint(lifted<LIFT>(a.x, s0, 0x1p-6f)), w1 = __float_as_uint(lifted<LIFT>(a.y, s1, 0x1p-6f));
-  const float2 lo = make_float2(lifted<LIFT>(__uint_as_float(w0 & 0xFFF00000u), s0, -0x1p-6f),
-                                lifted<LIFT>(__uint_as_float(w1 & 0xFFF00000u), s1, -0x1p-6f));
+__device__ __forceinline__ F2 round_r(F2 a, uint32_t bits0, uint32_t bits1) {
+  float2 x = un2(a), s;
+  if (LIFT) {
+    s = make_float2(below(x.x), below(x.y));
+    x = make_float2(fmaf(s.x, 0x1p-6f, x.x), fmaf(s.y, 0x1p-6f, x.y));
+  }
+  const uint32_t w0 = __float_as_uint(x.x), w1 = __float_as_uint(x.y);
+  F2 lo = f2(__uint_as_float(w0 & 0xFFF00000u), __uint_as_float(w1 & 0xFFF00000u));
+  if (LIFT) lo = fma2(f2(s), f2(-0x1p-6f), lo);
   // eight gaps between codes
-  const float2 gap8 = make_float2(__uint_as_float(w0 & 0x7F800000u), __uint_as_float(w1 & 0x7F800000u));
-  const float2 hi = make_float2(fmaf(gap8.x, 0.125f, lo.x), fmaf(gap8.y, 0.125f, lo.y));
+  const F2 gap8 = f2(__uint_as_float(w0 & 0x7F800000u), __uint_as_float(w1 & 0x7F800000u));
+  const F2 hi = fma2(gap8, f2(0.125f), lo);
   // bits / 2^19, from the significand of a number in [1/8, 1/4)
-  const F2 chance = f2(__uint_as_float(bits0 * 128 + 0x3E000000u) - 0.125f, __uint_as_float(bits1 * 128 + 0x3E000000u) - 0.125f);
-  const float2 p = un2((a2 - f2(lo)) * (a2 + f2(lo))), q = un2(chance * (f2(gap8) * (f2(lo) + f2(hi))));
-  return f2(p.x > q.x ? hi.x : lo.x, p.y > q.y ? hi.y : lo.y);
+  const F2 chance = f2(__uint_as_float(bits0 * 128 + 0x3E000000u), __uint_as_float(bits1 * 128 + 0x3E000000u)) - f2(0.125f);
+  const float2 p = un2((a - lo) * (a + lo)), q = un2(chance * (gap8 * (lo + hi)));
+  const float2 l = un2(lo), u = un2(hi);
+  return f2(p.x > q.x ? u.x : l.x, p.y > q.y ? u.y : l.y);
 }
 
-// The moments of a lane, m and r, to e4m3 values: im, ir are the scales' reciprocals.
+// The moments of a lane, m and -r, to e4m3 values: im, -ir are the scales' reciprocals.
 // first: what the lane's first element is hashed from, at(q) the q-th's distance from it.
 template <bool LIFT, class At>
-__device__ __forceinline__ void round_block(F2 (&m)[4], F2 (&r)[4], float im, float ir, uint32_t first, At at) {
+__device__ __forceinline__ void round_block(F2 (&m)[4], F2 (&r)[4], float im, float nir, uint32_t first, At at) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint32_t h0 = mix32(first + (uint32_t)at(2 * k) * 0x9E3779B1u);
     const uint32_t h1 = mix32(first + (uint32_t)at(2 * k + 1) * 0x9E3779B1u);
-    const float2 x = un2(m[k]);
-    m[k] = f2(copysignf(round_m<LIFT>(fabsf(x.x) * im, h0 & 0xFFFFu), x.x),
-              copysignf(round_m<LIFT>(fabsf(x.y) * im, h1 & 0xFFFFu), x.y));
-    r[k] = round_r<LIFT>(r[k] * f2(ir), h0 >> 16, h1 >> 16);
+    const float2 x = un2(m[k] * f2(im));
+    m[k] = f2(round_m<LIFT>(x.x, h0 & 0xFFFFu), round_m<LIFT>(x.y, h1 & 0xFFFFu));
+    r[k] = round_r<LIFT>(r[k] * f2(nir), h0 >> 16, h1 >> 16);
   }
 }
 
@@ -591,21 +600,6 @@ __device__ __forceinline__ float smallest(float a, F2 b) {
   return o;
 }
 
-// Loads that stay where they are written: all of a block's before the arithmetic.
-__device__ __forceinline__ void ld16(const void* p, F2& a, F2& b) {
-  asm volatile("ld.global.v2.b64 {%0, %1}, [%2];" : "=l"(a.v), "=l"(b.v) : "l"(p));
-}
-__device__ __forceinline__ uint2 ld8(const void* p) {
-  uint2 o;
-  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(o.x), "=r"(o.y) : "l"(p));
-  return o;
-}
-__device__ __forceinline__ uint32_t ld4(const void* p) {
-  uint32_t o;
-  asm volatile("ld.global.b32 %0, [%1];" : "=r"(o) : "l"(p));
-  return o;
-}
-
 // Two codes to floats and back; values of e4m3 convert exactly.
 __device__ __forceinline__ F2 code_values(uint32_t two) {
   return f2(__half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3))));
@@ -619,162 +613,267 @@ __device__ __forceinline__ uint32_t bf16_pair(F2 a) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// One warp steps one block: four pairs of elements a lane.  Whole: the block is full and
-// the pointers are aligned to four elements; lane l holds elements 4l..4l+3 of
-// either half.  Otherwise element 32 q + l is lane l's q-th, so that accesses of single elements
-// are those of neighbouring lanes to neighbouring addresses.
+// 32 bytes a lane.
+__device__ __forceinline__ void ld32(const void* p, F2 (&x)[4]) {
+  asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(x[0].v), "=l"(x[1].v), "=l"(x[2].v), "=l"(x[3].v) : "l"(p));
+}
+__device__ __forceinline__ void st32(void* p, const F2 (&x)[4]) {
+  asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(x[0].v), "l"(x[1].v), "l"(x[2].v), "l"(x[3].v) : "memory");
+}
+__device__ __forceinline__ uint4 ld16(const void* p) {
+  uint4 o;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(o.x), "=r"(o.y), "=r"(o.z), "=r"(o.w) : "l"(p));
+  return o;
+}
+__device__ __forceinline__ uint2 ld8(const void* p) {
+  uint2 o;
+  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(o.x), "=r"(o.y) : "l"(p));
+  return o;
+}
 
-// em, er: the scales' bytes, which come back as the new ones.
-template <bool BF16, bool WHOLE>
-__device__ __forceinline__ void step_block(const Update& u, int o, const AdamwState& st, const Hyper& h, int& em,
-                                           int& er) {
-  const int lane = threadIdx.x & 31;
-  const int64_t flat = u.c.flat + o;
-  const auto at = [&](int q) { return WHOLE ? 128 * (q >> 2) + 4 * lane + (q & 3) : 32 * q + lane; };
-  const auto in = [&](int q) { return WHOLE || o + at(q) < u.c.len; };
-  uint8_t *mq = st.mq + flat, *rq = st.rq + flat;
-  float* wp = u.w + o;
-  F2 w[4], g[4], m[4], r[4];
-  if (WHOLE) {
-    uint32_t cm[2], cr[2];
-    uint2 cg[2];
+// One block of one tensor, where its arrays are.
+struct Block {
+  float* w;
+  const char* g;
+  uint16_t* b;      // the bfloat16 copy, or null
+  uint8_t *mq, *rq;
+  int64_t flat;     // its first element in the flat state
+  int len;
+};
+// A warp steps one block, eight elements a lane.  Where the block is full and its pointers
+// are aligned to those of a lane, lane l has elements 8l..8l+7; otherwise element
+// 32 q + l is lane l's q-th, so that accesses of single elements are those of
+// neighbouring lanes to neighbouring addresses.
+template <bool BF16>
+__device__ __forceinline__ bool wide(const void* w, const void* g, const void* b) {
+  return ((reinterpret_cast<uintptr_t>(w) & 31) | (reinterpret_cast<uintptr_t>(g) & (BF16 ? 15 : 31)) |
+          (reinterpret_cast<uintptr_t>(b) & 15)) == 0;
+}
+
+__device__ __forceinline__ void codes_to(uint2 c, F2 (&x)[4]) {
+  x[0] = code_values(c.x);
+  x[1] = code_values(c.x >> 16);
+  x[2] = code_values(c.y);
+  x[3] = code_values(c.y >> 16);
+}
+__device__ __forceinline__ uint2 to_codes(const F2 (&x)[4]) {
+  return make_uint2(value_codes(x[0]) | (value_codes(x[1]) << 16), value_codes(x[2]) | (value_codes(x[3]) << 16));
+}
+__device__ __forceinline__ void bf16_to(uint4 c, F2 (&x)[4]) {
+  const uint32_t u[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int i = 128 * k + 4 * lane;
-      cm[k] = ld4(mq + i);
-      cr[k] = ld4(rq + i);
-      if (BF16) cg[k] = ld8(u.g + 2 * (o + i));
-      else ld16(u.g + 4 * (o + i), g[2 * k], g[2 * k + 1]);
-      ld16(wp + i, w[2 * k], w[2 * k + 1]);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      m[k] = code_values(cm[k >> 1] >> (16 * (k & 1)));
-      r[k] = code_values(cr[k >> 1] >> (16 * (k & 1)));
-      if (BF16) {
-        const uint32_t two = k & 1 ? cg[k >> 1].y : cg[k >> 1].x;
-        g[k] = f2(__uint_as_float(two << 16), __uint_as_float(two & 0xFFFF0000u));
-      }
-    }
-  } else {
-    float xw[8], xg[8];
-    uint32_t cm[8], cr[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      xw[q] = in(q) ? wp[at(q)] : 0.0f;
-      xg[q] = in(q) ? load1<BF16>(u.g, o + at(q)) : 0.0f;
-      cm[q] = mq[at(q)];
-      cr[q] = rq[at(q)];
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      w[k] = f2(xw[2 * k], xw[2 * k + 1]);
-      g[k] = f2(xg[2 * k], xg[2 * k + 1]);
-      m[k] = code_values(cm[2 * k] | (cm[2 * k + 1] << 8));
-      r[k] = code_values(cr[2 * k] | (cr[2 * k + 1] << 8));
-    }
-  }
+  for (int k = 0; k < 4; ++k) x[k] = f2(__uint_as_float(u[k] << 16), __uint_as_float(u[k] & 0xFFFF0000u));
+}
+
+// -sqrt(v) of nv = -v, correctly rounded like sqrtf: one Newton step on x^2 = v from
+// v * rsqrt(v), with the residual in one rounding (Markstein's).  Checked against sqrtf for every
+// float from 2^-100 to 2^127; v is in that range.  Two thirds of sqrtf's instructions saved.
+__device__ __forceinline__ F2 negative_root(F2 nv) {
+  const float2 x = un2(nv);
+  float a, b;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(a) : "f"(-x.x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(b) : "f"(-x.y));
+  const F2 y = f2(a, b), s = nv * y;
+  return fma2(fma2(s, s, nv), y * f2(0.5f), s);
+}
+
+// The arithmetic of one block: weights and gradients in w, g, codes' values in m, r and the
+// bytes of their scales in em, er; all but g come back as they are to be stored.
+// first: what the lane's first element is hashed from, from(q) the q-th's distance to it;
+// store(): writes the weights, between the step and the rounding.
+template <class From, class Store>
+__device__ __forceinline__ void step_moments(F2 (&w)[4], F2 (&g)[4], F2 (&m)[4], F2 (&r)[4], int& em, int& er,
+                                             const Factors& f, const Hyper& h, uint32_t first, From from, Store store) {
   // b1 (code * scale) is (b1 scale) code: the scale is a power of two
   const F2 b1ms = f2(h.beta1 * scale_of(em)), rs = f2(scale_of(er));
 #pragma unroll
-  for (int k = 0; k < 4; ++k) g[k] = g[k] * f2(u.coef);
-  if (u.huge) {
+  for (int k = 0; k < 4; ++k) g[k] = g[k] * f2(f.coef);
+  if (f.huge) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float2 x = un2(g[k]);
       g[k] = f2(limit(x.x), limit(x.y));
     }
   }
-  float mm = 0.0f, vm = 0.0f, ml = FLT_MAX, rl = FLT_MAX;
+  float mm = 0.0f, vm = 0.0f, ml = FLT_MAX, vl = FLT_MAX;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     m[k] = m[k] * b1ms + f2(h.omb1_2) * g[k];
     r[k] = r[k] * rs;
-    const F2 v = f2(h.beta2_2) * (r[k] * r[k]) + f2(h.omb2_2) * g[k] * g[k];
+    r[k] = f2(h.nbeta2_2) * (r[k] * r[k]) + f2(h.nomb2_2) * g[k] * g[k];   // -v
     mm = largest(mm, m[k]);
-    vm = largest(vm, v);
-    const float2 x = un2(v);
-    r[k] = f2(sqrtf(x.x), sqrtf(x.y));
     ml = smallest(ml, m[k]);
-    rl = smallest(rl, r[k]);
-    const float2 d = un2(fma2(r[k], f2(u.s.second), f2(h.eps_2)));
-    w[k] = fma2(w[k], f2(u.s.shrink), m[k] * f2(reciprocal(d.x), reciprocal(d.y)) * f2(-u.s.first));
+    vm = largest(vm, r[k]);
+    vl = smallest(vl, r[k]);
   }
-  if (WHOLE) {
+  if (__any_sync(0xffffffffu, vl < 0x1p-100f)) {   // zeros, above all
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int i = 128 * k + 4 * lane;
-      *reinterpret_cast<ulonglong2*>(wp + i) = make_ulonglong2(w[2 * k].v, w[2 * k + 1].v);
-      if (u.b) *reinterpret_cast<uint2*>(u.b + o + i) = make_uint2(bf16_pair(w[2 * k]), bf16_pair(w[2 * k + 1]));
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = un2(r[k]);
+      r[k] = f2(-sqrtf(-x.x), -sqrtf(-x.y));
     }
   } else {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if (!in(q)) continue;
-      const float2 two = un2(w[q >> 1]);
-      const float x = q & 1 ? two.y : two.x;
-      wp[at(q)] = x;
-      if (u.b) u.b[o + at(q)] = bf16_bits(x);
-    }
+    for (int k = 0; k < 4; ++k) r[k] = negative_root(r[k]);
   }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 d = un2(fma2(r[k], f2(-f.s.second), f2(h.eps_2)));
+    w[k] = fma2(w[k], f2(f.s.shrink), m[k] * f2(reciprocal(d.x), reciprocal(d.y)) * f2(-f.s.first));
+  }
+  store();
   // magnitudes order as their bits do, and roots as their squares
   em = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(mm)));
-  er = scale_byte(__float_as_uint(sqrtf(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vm))))));
+  er = root_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
   const float im = inverse_scale(em), ir = inverse_scale(er);
-  const uint32_t base = (uint32_t)flat * 0x9E3779B1u + (uint32_t)(flat >> 32) * 0x85EBCA77u + u.s.key;
-  const uint32_t first = base + (uint32_t)at(0) * 0x9E3779B1u;
-  const auto from = [&](int q) { return WHOLE ? 128 * (q >> 2) + (q & 3) : 32 * q; };
   // an element 2^15 below the block's largest: hardly ever, but for zeros
-  if (__any_sync(0xffffffffu, fminf(ml * im, rl * ir) < 0x1p-6f)) round_block<true>(m, r, im, ir, first, from);
-  else round_block<false>(m, r, im, ir, first, from);
-  if (WHOLE) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int i = 128 * k + 4 * lane;
-      *reinterpret_cast<uint32_t*>(mq + i) = value_codes(m[2 * k]) | (value_codes(m[2 * k + 1]) << 16);
-      *reinterpret_cast<uint32_t*>(rq + i) = value_codes(r[2 * k]) | (value_codes(r[2 * k + 1]) << 16);
-    }
+  if (__any_sync(0xffffffffu, ml * im < 0x1p-6f || vl * ir * ir < 0x1.1p-12f)) round_block<true>(m, r, im, -ir, first, from);
+  else round_block<false>(m, r, im, -ir, first, from);
+}
+
+// What the first element of a block is hashed from.
+__device__ __forceinline__ uint32_t hash_base(int64_t flat, uint32_t key) {
+  return (uint32_t)flat * 0x9E3779B1u + (uint32_t)(flat >> 32) * 0x85EBCA77u + key;
+}
+
+// A lane's eight elements as they lie in memory.
+template <bool BF16>
+struct Loaded {
+  F2 w[4], g[BF16 ? 1 : 4];
+  uint4 g16;
+  uint2 m, r;
+};
+template <bool BF16>
+__device__ __forceinline__ void step_loaded(Loaded<BF16>& x, const Block& b, int& em, int& er, const Factors& f,
+                                            const Hyper& h) {
+  const int lane = threadIdx.x & 31;
+  F2 g[4], m[4], r[4];
+  codes_to(x.m, m);
+  codes_to(x.r, r);
+  if (BF16) {
+    bf16_to(x.g16, g);
   } else {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {   // behind the tensor's end: zeros, as they were
-      mq[at(q)] = (uint8_t)(value_codes(m[q >> 1]) >> (8 * (q & 1)));
-      rq[at(q)] = (uint8_t)(value_codes(r[q >> 1]) >> (8 * (q & 1)));
+    for (int k = 0; k < 4; ++k) g[k] = x.g[BF16 ? 0 : k];
+  }
+  step_moments(x.w, g, m, r, em, er, f, h, hash_base(b.flat, f.s.key) + lane * 8 * 0x9E3779B1u, [](int q) { return q; },
+               [&] {
+                 st32(b.w + 8 * lane, x.w);
+                 if (b.b)
+                   *reinterpret_cast<uint4*>(b.b + 8 * lane) =
+                       make_uint4(bf16_pair(x.w[0]), bf16_pair(x.w[1]), bf16_pair(x.w[2]), bf16_pair(x.w[3]));
+               });
+  *reinterpret_cast<uint2*>(b.mq + 8 * lane) = to_codes(m);
+  *reinterpret_cast<uint2*>(b.rq + 8 * lane) = to_codes(r);
+}
+
+// em, er: the scales' bytes, which come back as the new ones.
+template <bool BF16>
+__device__ __forceinline__ void step_block(const Block& b, int& em, int& er, const Factors& f, const Hyper& h) {
+  const int lane = threadIdx.x & 31;
+  if (b.len == kQBlock && wide<BF16>(b.w, b.g, b.b)) {
+    Loaded<BF16> x;
+    ld32(b.w + 8 * lane, x.w);
+    if constexpr (BF16) x.g16 = ld16(b.g + 16 * lane);
+    else ld32(b.g + 32 * lane, x.g);
+    x.m = ld8(b.mq + 8 * lane);
+    x.r = ld8(b.rq + 8 * lane);
+    step_loaded<BF16>(x, b, em, er, f, h);
+    return;
+  }
+  float xw[8], xg[8];
+  uint32_t cm[8], cr[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int i = 32 * q + lane;
+    xw[q] = i < b.len ? b.w[i] : 0.0f;
+    xg[q] = i < b.len ? load1<BF16>(b.g, i) : 0.0f;
+    cm[q] = b.mq[i];
+    cr[q] = b.rq[i];
+  }
+  F2 w[4], g[4], m[4], r[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    w[k] = f2(xw[2 * k], xw[2 * k + 1]);
+    g[k] = f2(xg[2 * k], xg[2 * k + 1]);
+    m[k] = code_values(cm[2 * k] | (cm[2 * k + 1] << 8));
+    r[k] = code_values(cr[2 * k] | (cr[2 * k + 1] << 8));
+  }
+  step_moments(w, g, m, r, em, er, f, h, hash_base(b.flat, f.s.key) + lane * 0x9E3779B1u, [](int q) { return 32 * q; }, [&] {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int i = 32 * q + lane;
+      if (i >= b.len) continue;
+      const float2 two = un2(w[q >> 1]);
+      const float x = q & 1 ? two.y : two.x;
+      b.w[i] = x;
+      if (b.b) b.b[i] = bf16_bits(x);
     }
+  });
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {   // behind the tensor's end: zeros, as they were
+    b.mq[32 * q + lane] = (uint8_t)(value_codes(m[q >> 1]) >> (8 * (q & 1)));
+    b.rq[32 * q + lane] = (uint8_t)(value_codes(r[q >> 1]) >> (8 * (q & 1)));
   }
 }
 
-// Four CTAs an SM: three whose warps load their next block ahead took 932 us in place of 901 us
-// for 285M parameters.
+// The blocks of the flat state go to the warps in fours, the scales of which are one word.  (Single
+// bytes, written among other warps' reads of their sector, took half of the step.)  No warp
+// waits for another.
+//
+// The pointers in wp, gp, cp are those of the tensors less their offset in the flat state, so that
+// a tensor's number is all that a block has to look up.
 template <bool BF16, int K>
 __global__ void __launch_bounds__(kThreads, 4) adamw_8bit_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
                                                                  const __grid_constant__ Pointers<K> gp,
                                                                  const __grid_constant__ Pointers<K> cp, int copies,
-                                                                 int p0, int c0, AdamwState st,
+                                                                 int p0, int np, int q0, int nq, AdamwState st,
                                                                  const ListStep* step, Hyper h) {
-  // A chunk's scales are read and written together, 32 neighbouring bytes each, which for a
-  // chunk inside a tensor are one sector.  Written by one block's warp at a time, byte by byte
-  // among the others' reads of the same sector, they took half of the step: 2116 us in place of 975 us.
-  constexpr int kBlocks = kListChunk / kQBlock;
-  __shared__ uint8_t scales[2][kBlocks];
-  Update u;
-  update_of<BF16>(u, t, wp, gp, cp, copies, p0, c0);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t blk = u.c.flat / kQBlock;
-  const int blocks = (u.c.len + kQBlock - 1) / kQBlock;
-  const int ms = lane < blocks ? st.ms[blk + lane] : 0, rs = lane < blocks ? st.rs[blk + lane] : 0;
-  const int whole = u.aligned ? u.c.len / kQBlock : 0;
-  if (!pass_results(u, t, step)) return;
-  for (int i = warp; i < blocks; i += kListWarps) {
-    int em = __shfl_sync(0xffffffffu, ms, i), er = __shfl_sync(0xffffffffu, rs, i);
-    if (i < whole) step_block<BF16, true>(u, i * kQBlock, st, h, em, er);
-    else step_block<BF16, false>(u, i * kQBlock, st, h, em, er);
-    if (lane == 0) {
-      scales[0][i] = (uint8_t)em;
-      scales[1][i] = (uint8_t)er;
-    }
+  const int lane = threadIdx.x & 31;
+  // the fours in the reverse of the norm's order: the gradients that it read last are in L2
+  const int k = blockIdx.x * kListWarps + (threadIdx.x >> 5);
+  const int four = q0 + nq - 1 - k;
+  int p = k < nq ? t.fours[four] : -1;
+  wait_for_previous();
+  if (k >= nq) return;
+  Factors f;
+  f.coef = t.result->coef;
+  f.huge = !(t.result->norm * f.coef < kGradMax);   // no element exceeds the norm
+  uint32_t ms = reinterpret_cast<const uint32_t*>(st.ms)[four], rs = reinterpret_cast<const uint32_t*>(st.rs)[four];
+  int skip = 0;
+  if (p >= 0) {
+    skip = t.skip[p];
+    f.s = step[p];
+    if (skip) return;
   }
-  __syncthreads();
-  if (warp < 2 && lane < blocks) (warp ? st.rs : st.ms)[blk + lane] = scales[warp][lane];
+#pragma unroll 1
+  for (int j = 0; j < 4; ++j) {
+    Block b;
+    b.flat = (4 * (int64_t)four + j) * kQBlock;
+    b.len = kQBlock;
+    int own = p;
+    if (p < 0) {   // of several tensors, or one's end
+      if (4 * (int64_t)four + j >= t.nqblocks) break;
+      own = t.owner[4 * (int64_t)four + j];
+      if (own < p0 || own >= p0 + np || t.skip[own]) continue;
+      f.s = step[own];
+      b.len = (int)min((int64_t)kQBlock, t.ends[own] - b.flat);
+    }
+    b.w = static_cast<float*>(const_cast<void*>(wp.p[own - p0])) + b.flat;
+    b.g = static_cast<const char*>(gp.p[own - p0]) + b.flat * (BF16 ? 2 : 4);
+    b.b = copies ? static_cast<uint16_t*>(const_cast<void*>(cp.p[own - p0])) + b.flat : nullptr;
+    b.mq = st.mq + b.flat;
+    b.rq = st.rq + b.flat;
+    int em = ms >> (8 * j) & 255, er = rs >> (8 * j) & 255;
+    step_block<BF16>(b, em, er, f, h);
+    const uint32_t keep = ~(255u << (8 * j));
+    ms = (ms & keep) | (uint32_t)em << (8 * j);
+    rs = (rs & keep) | (uint32_t)er << (8 * j);
+  }
+  if (lane == 0) {
+    reinterpret_cast<uint32_t*>(st.ms)[four] = ms;
+    reinterpret_cast<uint32_t*>(st.rs)[four] = rs;
+  }
 }
 
 // ---------------- small lists ----------------
@@ -815,7 +914,8 @@ __device__ __forceinline__ double block_squares(const char* g, int len, bool& ba
   return warp_sum(sum);
 }
 
-// The sum over all CTAs of a value of each warp, and whether one of them is bad.
+// The sum over all CTAs of a value of each warp, and whether one of them is bad.  Every thread has
+// arrived at the cluster's barrier before.
 __device__ __forceinline__ double cluster_total(double warp_value, bool warp_bad, bool& bad, double* mine, int* mine_bad,
                                                 double* all, int* all_bad) {
   namespace cg = cooperative_groups;
@@ -825,6 +925,7 @@ __device__ __forceinline__ double cluster_total(double warp_value, bool warp_bad
     mine[warp] = warp_value;
     mine_bad[warp] = warp_bad;
   }
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
   __syncthreads();
   if (warp == 0) {
     const double s = warp_sum(lane < kSmallWarps ? mine[lane] : 0.0);
@@ -857,6 +958,8 @@ __global__ void __launch_bounds__(32 * kSmallWarps)
   const auto gradient = [&](const ListChunk& c) {
     return static_cast<const char*>(gp.p[c.param]) + c.start * (BF16 ? 2 : 4);
   };
+  // shared memory of another CTA may be written once that has started: waited for in cluster_total
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
   if (threadIdx.x == 0) skipped = 0;
   double sum = 0.0;
   bool bad = false;
@@ -881,35 +984,46 @@ __global__ void __launch_bounds__(32 * kSmallWarps)
       if (__ldcg(&t.mark[c.param]) != pass) sum += s;
     }
     bool unused;
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     sum = cluster_total(sum, false, unused, sums, bads, all[1], all_bad[1]);
   }
   const double norm = sqrt(sum);
   const float coef = max_norm > 0.0 && norm > max_norm ? (float)(max_norm / norm) : 1.0f;
   if (OP != kOpNorm && (OP != kOpClip || coef != 1.0f)) {
     for (int b = b0; b < t.nblocks; b += warps) {
-      Update u;
-      u.c = t.blocks[b];
-      if (__ldcg(&t.mark[u.c.param]) == pass) continue;
-      u.g = gradient(u.c);
+      const ListChunk c = t.blocks[b];
+      if (__ldcg(&t.mark[c.param]) == pass) continue;
       if (OP == kOpClip) {
-        void* g = const_cast<char*>(u.g);
-        for (int i = lane; i < u.c.len; i += 32) store1<BF16>(g, i, load1<BF16>(g, i) * coef);
+        void* g = const_cast<char*>(gradient(c));
+        for (int i = lane; i < c.len; i += 32) store1<BF16>(g, i, load1<BF16>(g, i) * coef);
         continue;
       }
-      u.w = static_cast<float*>(const_cast<void*>(wp.p[u.c.param])) + u.c.start;
-      u.b = copies ? static_cast<uint16_t*>(const_cast<void*>(cp.p[u.c.param])) + u.c.start : nullptr;
-      u.aligned = aligned4<false>(u.w) && aligned4<BF16>(u.g) && aligned4<true>(u.b);
-      const float4 f = __ldcg(reinterpret_cast<const float4*>(adv.out + u.c.param));
-      u.s = ListStep{f.x, f.y, f.z, __float_as_uint(f.w)};
-      u.coef = coef;
-      u.huge = !(norm * coef < (double)kGradMax);
+      const float4 s = __ldcg(reinterpret_cast<const float4*>(adv.out + c.param));
+      Factors f;
+      f.s = ListStep{s.x, s.y, s.z, __float_as_uint(s.w)};
+      f.coef = coef;
+      f.huge = !(norm * coef < (double)kGradMax);
+      Block k;
+      k.w = static_cast<float*>(const_cast<void*>(wp.p[c.param])) + c.start;
+      k.g = gradient(c);
+      k.b = copies ? static_cast<uint16_t*>(const_cast<void*>(cp.p[c.param])) + c.start : nullptr;
+      k.mq = st.mq + c.flat;
+      k.rq = st.rq + c.flat;
+      k.flat = c.flat;
+      k.len = c.len;
       if (OP == kOpF32) {
-        step_run<BF16>(u, st.m + u.c.flat, st.v + u.c.flat, lane, 32, h, [] { return true; });
+        Update u;
+        u.c = c;
+        u.w = k.w;
+        u.g = k.g;
+        u.b = k.b;
+        u.aligned = aligned4<false>(u.w) && aligned4<BF16>(u.g) && aligned4<true>(u.b);
+        u.f = f;
+        step_run<BF16>(u, st.m + c.flat, st.v + c.flat, lane, 32, h, [] { return true; });
       } else {
-        const int64_t blk = u.c.flat / kQBlock;
+        const int64_t blk = c.flat / kQBlock;
         int em = st.ms[blk], er = st.rs[blk];
-        if (u.aligned && u.c.len == kQBlock) step_block<BF16, true>(u, 0, st, h, em, er);
-        else step_block<BF16, false>(u, 0, st, h, em, er);
+        step_block<BF16>(k, em, er, f, h);
         if (lane == 0) {
           st.ms[blk] = (uint8_t)em;
           st.rs[blk] = (uint8_t)er;
@@ -1045,7 +1159,7 @@ cudaError_t launch_list_scale(const ListTables& t, void* const* g, int p0, int n
 }
 
 cudaError_t launch_adamw(const ListTables& t, float* const* w, const void* const* g, void* const* copies, int p0,
-                         int np, int c0, int nc, int bf16, int eight, const AdamwState& st, const ListStep* step,
+                         int np, int c0, int nc, int bf16, const AdamwState& st, const ListStep* step,
                          float beta1, float omb1, float beta2, float omb2, float eps, cudaStream_t s) {
   const Hyper h = hyper(beta1, omb1, beta2, omb2, eps);
   return by_count(np, [&](auto n) {
@@ -1054,9 +1168,29 @@ cudaError_t launch_adamw(const ListTables& t, float* const* w, const void* const
     const Pointers<K> ag = pack<K>(g + p0, np);
     const Pointers<K> ac = copies ? pack<K>(const_cast<const void* const*>(copies) + p0, np) : Pointers<K>{};
     const int cc = copies != nullptr;
-    auto* kernel = eight ? (bf16 ? adamw_8bit_kernel<true, K> : adamw_8bit_kernel<false, K>)
-                         : (bf16 ? adamw_f32_kernel<true, K> : adamw_f32_kernel<false, K>);
-    return launch_early(kernel, nc, s, t, aw, ag, ac, cc, p0, c0, st, step, h);
+    return launch_early(bf16 ? adamw_f32_kernel<true, K> : adamw_f32_kernel<false, K>, nc, s, t, aw, ag, ac, cc, p0, c0, st,
+                        step, h);
+  });
+}
+
+cudaError_t launch_adamw_8bit(const ListTables& t, float* const* w, const void* const* g, void* const* copies,
+                              const int64_t* offset, int p0, int np, int q0, int nq, int bf16, const AdamwState& st,
+                              const ListStep* step, float beta1, float omb1, float beta2, float omb2, float eps,
+                              cudaStream_t s) {
+  const Hyper h = hyper(beta1, omb1, beta2, omb2, eps);
+  return by_count(np, [&](auto n) {
+    constexpr int K = decltype(n)::value;
+    // less the tensor's offset in the flat state
+    const auto less = [&](auto* const* p, int size) {
+      Pointers<K> a;
+      for (int i = 0; i < np; ++i)
+        a.p[i] = reinterpret_cast<const void*>(reinterpret_cast<uintptr_t>(p[p0 + i]) - (uintptr_t)offset[p0 + i] * size);
+      return a;
+    };
+    const Pointers<K> aw = less(w, 4), ag = less(g, bf16 ? 2 : 4), ac = copies ? less(copies, 2) : Pointers<K>{};
+    const int ctas = (nq + kListWarps - 1) / kListWarps;
+    return launch_early(bf16 ? adamw_8bit_kernel<true, K> : adamw_8bit_kernel<false, K>, ctas, s, t, aw, ag, ac,
+                        (int)(copies != nullptr), p0, np, q0, nq, st, step, h);
   });
 }
 

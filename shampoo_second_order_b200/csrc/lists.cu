@@ -93,7 +93,7 @@ shampoo_status check_list(int nparams, const int64_t* numel, int grad_dtype) {
   for (int i = 0; i < nparams; ++i) {
     if (numel[i] < 1 || numel[i] > (int64_t(1) << 40))
       return refuse(nullptr, SHAMPOO_EINVAL, "bad element count for parameter " + std::to_string(i));
-    total += (numel[i] + kListChunk - 1) / kListChunk + 1;   // chunks
+    total += (numel[i] + kListChunk - 1) / kListChunk;   // chunks
     if (total > (int64_t(1) << 30)) return refuse(nullptr, SHAMPOO_EINVAL, "more elements than a list can hold");
   }
   return SHAMPOO_OK;
@@ -109,15 +109,8 @@ shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dt
   for (int i = 0; i < nparams; ++i) {
     if (i % kListGroup == 0) l->groups.push_back(Group{i, 0, (int)chunks.size(), 0, 0});
     l->offset.push_back(l->total);
-    for (int64_t s = 0; s < numel[i];) {
-      ListChunk c{};
-      c.param = i;
-      c.start = s;
-      c.flat = l->total + s;
-      c.len = (int)std::min<int64_t>(kListChunk - c.flat % kListChunk, numel[i] - s);
-      chunks.push_back(c);
-      s += c.len;
-    }
+    for (int64_t s = 0; s < numel[i]; s += kListChunk)
+      chunks.push_back(ListChunk{i, (int)std::min<int64_t>(kListChunk, numel[i] - s), s, l->total + s});
     l->total += (numel[i] + kQBlock - 1) / kQBlock * kQBlock;
     Group& g = l->groups.back();
     g.np = i + 1 - g.p0;
@@ -151,6 +144,38 @@ shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dt
   if (e == cudaSuccess && db)
     e = cudaMemcpyAsync(db, blocks.data(), blocks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
   if (e != cudaSuccess) return cuda_error(l, e, "upload of the chunk table");
+  return SHAMPOO_OK;
+}
+
+// The tables of the 8-bit step: which tensor each block of the flat state belongs to.
+shampoo_status make_blocks(List* l) {
+  const int n = (int)l->numel.size();
+  const int64_t blocks = l->total / kQBlock;
+  std::vector<int> owner(blocks), fours((blocks + 3) / 4);
+  std::vector<int64_t> ends(n);
+  for (int i = 0; i < n; ++i) {
+    ends[i] = l->offset[i] + l->numel[i];
+    const int64_t b0 = l->offset[i] / kQBlock, b1 = (ends[i] + kQBlock - 1) / kQBlock;
+    std::fill(owner.begin() + b0, owner.begin() + b1, i);
+  }
+  for (int64_t q = 0; q < (int64_t)fours.size(); ++q) {
+    const int p = owner[4 * q];
+    fours[q] = (4 * q + 4) * kQBlock <= ends[p] ? p : -1;
+  }
+  int *d_owner = nullptr, *d_fours = nullptr;
+  int64_t* d_ends = nullptr;
+  cudaError_t e = zeroed(l, &d_owner, blocks);
+  if (e == cudaSuccess) e = zeroed(l, &d_fours, (int64_t)fours.size());
+  if (e == cudaSuccess) e = zeroed(l, &d_ends, n);
+  if (e != cudaSuccess) return refuse(l, SHAMPOO_ENOMEM, std::string("device allocation failed: ") + cudaGetErrorString(e));
+  e = cudaMemcpyAsync(d_owner, owner.data(), owner.size() * sizeof(int), cudaMemcpyHostToDevice, l->stream);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(d_fours, fours.data(), fours.size() * sizeof(int), cudaMemcpyHostToDevice, l->stream);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(d_ends, ends.data(), n * sizeof(int64_t), cudaMemcpyHostToDevice, l->stream);
+  if (e != cudaSuccess) return cuda_error(l, e, "upload of the block tables");
+  l->tab.owner = d_owner;
+  l->tab.fours = d_fours;
+  l->tab.ends = d_ends;
+  l->tab.nqblocks = blocks;
   return SHAMPOO_OK;
 }
 
@@ -381,10 +406,12 @@ shampoo_status shampoo_adamw_create(shampoo_adamw** out, int nparams, const int6
       } else {
         if (e == cudaSuccess) e = zeroed(l, &a->st.mq, l->total);
         if (e == cudaSuccess) e = zeroed(l, &a->st.rq, l->total);
-        if (e == cudaSuccess) e = zeroed(l, &a->st.ms, l->total / kQBlock);
-        if (e == cudaSuccess) e = zeroed(l, &a->st.rs, l->total / kQBlock);
+        const int64_t words = (l->total / kQBlock + 3) / 4;   // read and written by the word
+        if (e == cudaSuccess) e = zeroed(l, &a->st.ms, 4 * words);
+        if (e == cudaSuccess) e = zeroed(l, &a->st.rs, 4 * words);
       }
       if (e != cudaSuccess) st = refuse(l, SHAMPOO_ENOMEM, std::string("device allocation failed: ") + cudaGetErrorString(e));
+      else if (state_bits == 8 && !l->tab.blocks) st = make_blocks(l);
     }
     if (st == SHAMPOO_OK) {
       cudaError_t e = cudaSuccess;
@@ -417,20 +444,30 @@ shampoo_status shampoo_adamw_step(shampoo_adamw* adamw, float* const* params, co
     if (st != SHAMPOO_OK) return st;
     OnDevice on(l->device);
     const ListAdvance adv{a->step, a->factors, a->decay, lr, a->beta1, a->beta2, (uint32_t)a->seed, (uint32_t)(a->seed >> 32)};
-    const float b1 = (float)a->beta1, omb1 = (float)(1.0 - a->beta1), b2 = (float)a->beta2, omb2 = (float)(1.0 - a->beta2);
+    const float b1f = (float)a->beta1, omb1 = (float)(1.0 - a->beta1), b2f = (float)a->beta2, omb2 = (float)(1.0 - a->beta2);
     cudaError_t e = cudaSuccess;
     if (l->tab.blocks) {
-      e = launch_adamw_small(l->tab, params, grads, copies, l->bf16, a->bits == 8, a->max_norm, adv, a->st, b1, omb1, b2,
+      e = launch_adamw_small(l->tab, params, grads, copies, l->bf16, a->bits == 8, a->max_norm, adv, a->st, b1f, omb1, b2f,
                              omb2, (float)a->eps, l->stream);
       return e == cudaSuccess ? SHAMPOO_OK : cuda_error(l, e, "adamw_small");
     }
     for (const Group& g : l->groups)
       if ((e = launch_list_norm(l->tab, grads, g.p0, g.np, g.c0, g.nc, g.b0, l->bf16, a->max_norm, adv, l->stream)) != cudaSuccess)
         return cuda_error(l, e, "list_norm");
-    for (const Group& g : l->groups)
-      if ((e = launch_adamw(l->tab, params, grads, copies, g.p0, g.np, g.c0, g.nc, l->bf16, a->bits == 8, a->st, a->factors,
-                            b1, omb1, b2, omb2, (float)a->eps, l->stream)) != cudaSuccess)
-        return cuda_error(l, e, "adamw");
+    for (const Group& g : l->groups) {
+      if (a->bits == 8) {
+        const int64_t b0 = l->offset[g.p0] / kQBlock;
+        const int last = g.p0 + g.np - 1;
+        const int64_t b1 = (l->offset[last] + l->numel[last] + kQBlock - 1) / kQBlock;
+        const int q0 = (int)(b0 / 4), q1 = (int)((b1 + 3) / 4);
+        e = launch_adamw_8bit(l->tab, params, grads, copies, l->offset.data(), g.p0, g.np, q0, q1 - q0, l->bf16, a->st,
+                              a->factors, b1f, omb1, b2f, omb2, (float)a->eps, l->stream);
+      } else {
+        e = launch_adamw(l->tab, params, grads, copies, g.p0, g.np, g.c0, g.nc, l->bf16, a->st, a->factors, b1f, omb1, b2f,
+                         omb2, (float)a->eps, l->stream);
+      }
+      if (e != cudaSuccess) return cuda_error(l, e, "adamw");
+    }
     return SHAMPOO_OK;
   });
 }

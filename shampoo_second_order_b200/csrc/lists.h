@@ -13,8 +13,7 @@ constexpr int kListWarps = 8;      // warps per CTA of the list kernels
 constexpr int kQBlock = 256;       // elements per scale of the 8-bit moments; every
                                    // tensor's state starts at a multiple of it
 
-// A contiguous run of one tensor's elements that lies between two multiples of
-// kListChunk in the flat state (so that the scales of its blocks lie in one 32-byte sector).
+// A contiguous run of one tensor's elements, at most kListChunk of them.
 struct ListChunk {
   int param;
   int len;
@@ -59,6 +58,11 @@ struct ListTables {
   ListResult* result;
   const ListChunk* blocks;   // of a small list: its blocks of kQBlock elements, else null
   int nblocks;
+  // 8-bit moments: the blocks of the flat state
+  const int* owner;          // [nqblocks] a block's tensor
+  const int* fours;          // [ceil(nqblocks / 4)] the tensor that has all of four blocks, full, or -1
+  const int64_t* ends;       // [n] where a tensor ends in the flat state
+  int64_t nqblocks;
   int nchunks, nparams;
   int nctas;              // of the pass, over all its launches
 };
@@ -88,7 +92,12 @@ cudaError_t launch_list_norm(const ListTables& t, const void* const* g, int p0, 
 cudaError_t launch_list_scale(const ListTables& t, void* const* g, int p0, int np, int c0, int nc, int bf16,
                               cudaStream_t s);
 cudaError_t launch_adamw(const ListTables& t, float* const* w, const void* const* g, void* const* copies, int p0,
-                         int np, int c0, int nc, int bf16, int eight, const AdamwState& st, const ListStep* step,
+                         int np, int c0, int nc, int bf16, const AdamwState& st, const ListStep* step,
                          float beta1, float omb1, float beta2, float omb2, float eps, cudaStream_t s);
+// The 8-bit step of the same tensors, whose blocks are among the fours [q0, q0 + nq).
+cudaError_t launch_adamw_8bit(const ListTables& t, float* const* w, const void* const* g, void* const* copies,
+                              const int64_t* offset, int p0, int np, int q0, int nq, int bf16, const AdamwState& st,
+                              const ListStep* step, float beta1, float omb1, float beta2, float omb2, float eps,
+                              cudaStream_t s);
 
 }  // namespace shampoo

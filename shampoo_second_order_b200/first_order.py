@@ -65,14 +65,19 @@ class _List:
 
     def _pointers(self, ts, what, dtype):
         """The C array of a list's device pointers, after its checks."""
-        ts = list(ts)
-        if len(ts) != len(self._numel):
-            raise ValueError(f"expected {len(self._numel)} {what}, got {len(ts)}")
-        if list(map(Tensor.numel, ts)) != self._numel or not all(map(Tensor.is_contiguous, ts)) \
-                or set(map(_dtype, ts)) != {dtype} or set(map(Tensor.get_device, ts)) != {self._device}:
-            raise ValueError(f"{what} must be contiguous {dtype} tensors of the given shapes "
-                             f"on CUDA device {self._device}")
-        return (C.c_void_p * len(ts)).from_buffer(array("Q", map(Tensor.data_ptr, ts)))
+        ts, n = list(ts), len(self._numel)
+        if len(ts) != n:
+            raise ValueError(f"expected {n} {what}, got {len(ts)}")
+        device = self._device
+        if n < 8:   # 1 us a tensor in place of 2.4 us for the first
+            fit = all([t.dtype is dtype and t.is_contiguous() and t.get_device() == device for t in ts]) \
+                and [t.numel() for t in ts] == self._numel
+        else:       # 0.33 us a tensor in place of 0.46 us
+            fit = set(map(_dtype, ts)) == {dtype} and all(map(Tensor.is_contiguous, ts)) \
+                and set(map(Tensor.get_device, ts)) == {device} and list(map(Tensor.numel, ts)) == self._numel
+        if not fit:
+            raise ValueError(f"{what} must be contiguous {dtype} tensors of the given shapes on CUDA device {device}")
+        return (C.c_void_p * n).from_buffer(array("Q", map(Tensor.data_ptr, ts)))
 
     def _on_stream(self, set_stream, call, *args):
         """call(context, *args) in the order of the caller's current stream."""
