@@ -26,7 +26,8 @@ namespace {
 // A run of at most kListGroup tensors and of their chunks: one launch of each kernel.
 struct Group {
   int p0, np, c0, nc;
-  int b0;   // first of its CTAs in the pass over the gradients
+  int g0, ng;   // gradient chunks
+  int b0;       // first of its CTAs in the pass over the gradients
 };
 
 // The list itself, common to both contexts.
@@ -105,16 +106,20 @@ shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dt
   cudaError_t e = cudaGetDevice(&l->device);
   if (e != cudaSuccess) return cuda_error(l, e, "cudaGetDevice");
   l->numel.assign(numel, numel + nparams);
-  std::vector<ListChunk> chunks, blocks;
+  std::vector<ListChunk> chunks, gchunks, blocks;
+  const int grad_chunk = kGradChunk / (l->bf16 ? 2 : 4);
   for (int i = 0; i < nparams; ++i) {
-    if (i % kListGroup == 0) l->groups.push_back(Group{i, 0, (int)chunks.size(), 0, 0});
+    if (i % kListGroup == 0) l->groups.push_back(Group{i, 0, (int)chunks.size(), 0, (int)gchunks.size(), 0, 0});
     l->offset.push_back(l->total);
     for (int64_t s = 0; s < numel[i]; s += kListChunk)
       chunks.push_back(ListChunk{i, (int)std::min<int64_t>(kListChunk, numel[i] - s), s, l->total + s});
+    for (int64_t s = 0; s < numel[i]; s += grad_chunk)
+      gchunks.push_back(ListChunk{i, (int)std::min<int64_t>(grad_chunk, numel[i] - s), s, l->total + s});
     l->total += (numel[i] + kQBlock - 1) / kQBlock * kQBlock;
     Group& g = l->groups.back();
     g.np = i + 1 - g.p0;
     g.nc = (int)chunks.size() - g.c0;
+    g.ng = (int)gchunks.size() - g.g0;
   }
   if (l->total <= (int64_t)kSmallBlocks * kQBlock) {
     for (int i = 0; i < nparams; ++i)
@@ -123,24 +128,28 @@ shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dt
     l->tab.nblocks = (int)blocks.size();
   }
   l->tab.nchunks = (int)chunks.size();
+  l->tab.ngchunks = (int)gchunks.size();
   l->tab.nparams = nparams;
-  ListChunk *d = nullptr, *db = nullptr;
+  ListChunk *d = nullptr, *dg = nullptr, *db = nullptr;
   for (Group& g : l->groups) {
     g.b0 = l->tab.nctas;
-    l->tab.nctas += list_norm_ctas(g.nc);
+    l->tab.nctas += list_norm_ctas(g.ng);
   }
-  if ((e = zeroed(l, &d, l->tab.nchunks)) != cudaSuccess ||
-      (!blocks.empty() && (e = zeroed(l, &db, l->tab.nblocks)) != cudaSuccess) || (e = zeroed(l, &l->tab.partial, l->tab.nchunks)) != cudaSuccess ||
+  if ((e = zeroed(l, &d, l->tab.nchunks)) != cudaSuccess || (e = zeroed(l, &dg, l->tab.ngchunks)) != cudaSuccess ||
+      (!blocks.empty() && (e = zeroed(l, &db, l->tab.nblocks)) != cudaSuccess) || (e = zeroed(l, &l->tab.partial, l->tab.ngchunks)) != cudaSuccess ||
       (e = zeroed(l, &l->tab.csum, l->tab.nctas)) != cudaSuccess ||
       (e = zeroed(l, &l->tab.mark, nparams)) != cudaSuccess || (e = zeroed(l, &l->tab.skip, nparams)) != cudaSuccess || (e = zeroed(l, &l->tab.result, 1)) != cudaSuccess)
     return refuse(l, SHAMPOO_ENOMEM, std::string("device allocation failed: ") + cudaGetErrorString(e));
   l->tab.chunks = d;
+  l->tab.gchunks = dg;
   l->tab.blocks = db;
   // pageable sources: staged by the driver before the calls return
   const ListResult first{0.f, 1.f, 0, 0, 1, 0};
   e = cudaMemcpyAsync(l->tab.result, &first, sizeof(first), cudaMemcpyHostToDevice, l->stream);
   if (e == cudaSuccess)
     e = cudaMemcpyAsync(d, chunks.data(), chunks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
+  if (e == cudaSuccess)
+    e = cudaMemcpyAsync(dg, gchunks.data(), gchunks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
   if (e == cudaSuccess && db)
     e = cudaMemcpyAsync(db, blocks.data(), blocks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
   if (e != cudaSuccess) return cuda_error(l, e, "upload of the chunk table");
@@ -306,7 +315,7 @@ shampoo_status shampoo_clip_norm(shampoo_clip* clip, const void* const* grads) {
       return e == cudaSuccess ? SHAMPOO_OK : cuda_error(l, e, "list_small");
     }
     for (const Group& g : l->groups) {
-      const cudaError_t e = launch_list_norm(l->tab, grads, g.p0, g.np, g.c0, g.nc, g.b0, l->bf16, 0.0, ListAdvance{}, l->stream);
+      const cudaError_t e = launch_list_norm(l->tab, grads, g.p0, g.np, g.g0, g.ng, g.b0, l->bf16, 0.0, ListAdvance{}, l->stream);
       if (e != cudaSuccess) return cuda_error(l, e, "list_norm");
     }
     return SHAMPOO_OK;
@@ -330,10 +339,10 @@ shampoo_status shampoo_clip_apply(shampoo_clip* clip, void* const* grads, double
       return e == cudaSuccess ? SHAMPOO_OK : cuda_error(l, e, "list_small");
     }
     for (const Group& g : l->groups)
-      if ((e = launch_list_norm(l->tab, g0, g.p0, g.np, g.c0, g.nc, g.b0, l->bf16, max_norm, ListAdvance{}, l->stream)) != cudaSuccess)
+      if ((e = launch_list_norm(l->tab, g0, g.p0, g.np, g.g0, g.ng, g.b0, l->bf16, max_norm, ListAdvance{}, l->stream)) != cudaSuccess)
         return cuda_error(l, e, "list_norm");
     for (const Group& g : l->groups)
-      if ((e = launch_list_scale(l->tab, grads, g.p0, g.np, g.c0, g.nc, l->bf16, l->stream)) != cudaSuccess)
+      if ((e = launch_list_scale(l->tab, grads, g.p0, g.np, g.g0, g.ng, l->bf16, l->stream)) != cudaSuccess)
         return cuda_error(l, e, "list_scale");
     return SHAMPOO_OK;
   });
@@ -452,7 +461,7 @@ shampoo_status shampoo_adamw_step(shampoo_adamw* adamw, float* const* params, co
       return e == cudaSuccess ? SHAMPOO_OK : cuda_error(l, e, "adamw_small");
     }
     for (const Group& g : l->groups)
-      if ((e = launch_list_norm(l->tab, grads, g.p0, g.np, g.c0, g.nc, g.b0, l->bf16, a->max_norm, adv, l->stream)) != cudaSuccess)
+      if ((e = launch_list_norm(l->tab, grads, g.p0, g.np, g.g0, g.ng, g.b0, l->bf16, a->max_norm, adv, l->stream)) != cudaSuccess)
         return cuda_error(l, e, "list_norm");
     for (const Group& g : l->groups) {
       if (a->bits == 8) {

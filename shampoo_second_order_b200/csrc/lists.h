@@ -6,18 +6,19 @@
 
 namespace shampoo {
 
-constexpr int kListChunk = 8192;   // elements per CTA of the list kernels
+constexpr int kListChunk = 8192;   // elements per CTA of the float32 step
+constexpr int kGradChunk = 32768;  // bytes of gradients that a CTA has in flight
 constexpr int kSmallBlocks = 512;  // of the lists that one cluster does
 constexpr int kSmallCtas = 8;
 constexpr int kListWarps = 8;      // warps per CTA of the list kernels
 constexpr int kQBlock = 256;       // elements per scale of the 8-bit moments; every
                                    // tensor's state starts at a multiple of it
 
-// A contiguous run of one tensor's elements, at most kListChunk of them.
+// A contiguous run of one tensor's elements.
 struct ListChunk {
   int param;
   int len;
-  int64_t start;   // first element inside the tensor, a multiple of kQBlock
+  int64_t start;   // first element inside the tensor, a multiple of 256
   int64_t flat;    // first element in the flat state, a multiple of kQBlock
 };
 
@@ -50,8 +51,9 @@ struct ListAdvance {
 
 // The tables of a pass over the gradients.
 struct ListTables {
-  const ListChunk* chunks;
-  double* partial;        // [nchunks] sums of squares of runs of a tensor's chunks, with the run's last
+  const ListChunk* chunks;   // of kListChunk elements
+  const ListChunk* gchunks;  // of kGradChunk bytes of gradients
+  double* partial;        // [ngchunks] sums of squares of runs of a tensor's chunks, with the run's last
   double* csum;           // [nctas] and of all that a CTA of the pass has read
   unsigned* mark;         // [n] the last pass that met an element of it that is not finite
   int* skip;              // [n] 1: the tensor's gradient was not finite
@@ -63,7 +65,7 @@ struct ListTables {
   const int* fours;          // [ceil(nqblocks / 4)] the tensor that has all of four blocks, full, or -1
   const int64_t* ends;       // [n] where a tensor ends in the flat state
   int64_t nqblocks;
-  int nchunks, nparams;
+  int nchunks, ngchunks, nparams;
   int nctas;              // of the pass, over all its launches
 };
 
@@ -85,7 +87,7 @@ cudaError_t launch_adamw_small(const ListTables& t, float* const* w, const void*
 
 // CTAs of the norm's launch over nc chunks.
 int list_norm_ctas(int nc);
-// The norm of the tensors [p0, p0 + np), whose chunks are [c0, c0 + nc), by CTAs that are the
+// The norm of the tensors [p0, p0 + np), whose gradient chunks are [c0, c0 + nc), by CTAs that are the
 // pass's b0th and following; the CTA that finishes last closes the pass over all chunks.
 cudaError_t launch_list_norm(const ListTables& t, const void* const* g, int p0, int np, int c0, int nc, int b0, int bf16,
                              double max_norm, const ListAdvance& adv, cudaStream_t s);
