@@ -162,6 +162,10 @@ __device__ void step_factors(const ListAdvance& adv, int p) {
 // the others, the clipping factor and each tensor's t.  One CTA, fixed order:
 // the same gradients give the same bits.
 __device__ void close_pass(const ListTables& t, unsigned pass, double max_norm, const ListAdvance& adv, double* red) {
+  // all loads of the usual case at once: it is the gradient pass's tail
+  const bool any = __ldcg(&t.result->bad) == pass;
+  double sum = 0.0;
+  for (int b = threadIdx.x; b < t.nctas; b += blockDim.x) sum += __ldcg(&t.csum[b]);
   int skipped = 0;
   for (int p = threadIdx.x; p < t.nparams; p += blockDim.x) {
     const int sk = __ldcg(&t.mark[p]) == pass;
@@ -169,24 +173,22 @@ __device__ void close_pass(const ListTables& t, unsigned pass, double max_norm, 
     skipped += sk;
     if (adv.step && !sk) adv.step[p] += 1;
   }
-  __syncthreads();
-  double sum = 0.0;
-  if (__ldcg(&t.result->bad) != pass) {
-    for (int b = threadIdx.x; b < t.nctas; b += blockDim.x) sum += __ldcg(&t.csum[b]);
-  } else {   // without the skipped tensors' chunks
+  if (any) {   // without the skipped tensors' chunks
+    __syncthreads();
+    sum = 0.0;
 #pragma unroll 8
     for (int i = threadIdx.x; i < t.ngchunks; i += blockDim.x) {
       const double x = __ldcg(&t.partial[i]);
       sum += t.skip[t.gchunks[i].param] ? 0.0 : x;
     }
+    skipped = (int)block_sum((double)skipped, red);
   }
   sum = block_sum(sum, red);
-  const double all = block_sum((double)skipped, red);
   if (threadIdx.x == 0) {
     const double norm = sqrt(sum);
     t.result->norm = (float)norm;
     t.result->coef = max_norm > 0.0 && norm > max_norm ? (float)(max_norm / norm) : 1.0f;
-    t.result->skipped = (int)all;
+    t.result->skipped = skipped;   // thread 0's share is none where no tensor is skipped
     t.result->done = 0;
     t.result->pass = pass + 1;
   }
@@ -270,12 +272,13 @@ __global__ void __launch_bounds__(kThreads, 4) list_norm_kernel(ListTables t, co
   __syncthreads();
   if (threadIdx.x == 0) {
     t.csum[b0 + blockIdx.x] = total;
-    __threadfence();
-    last = atomicAdd(&t.result->done, 1u) == (unsigned)t.nctas - 1;
+    // releases what this CTA has written, and acquires what those before it have
+    unsigned done;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(done) : "l"(&t.result->done) : "memory");
+    last = done == (unsigned)t.nctas - 1;
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
   close_pass(t, pass, max_norm, adv, red);
 }
 
