@@ -284,9 +284,16 @@ def shampoo_selftest_stall_next_apply(ctx):
     return _check(lib().shampoo_selftest_stall_next_apply(ctx), ctx)
 
 
-def _check_of(error_of, st, ctx):
+def _check_clip(st, ctx):
     if st != OK:
-        msg = error_of(ctx)
+        msg = lib().shampoo_clip_last_error(ctx)
+        raise ShampooError(st, msg.decode() if msg else "")
+    return st
+
+
+def _check_adamw(st, ctx):
+    if st != OK:
+        msg = lib().shampoo_adamw_last_error(ctx)
         raise ShampooError(st, msg.decode() if msg else "")
     return st
 
@@ -305,28 +312,27 @@ def shampoo_clip_create(numel, grad_dtype=F32, stream=0):
 
 
 def shampoo_clip_norm(ctx, grads):
-    return _check_of(lib().shampoo_clip_last_error, lib().shampoo_clip_norm(ctx, grads), ctx)
+    return _check_clip(lib().shampoo_clip_norm(ctx, grads), ctx)
 
 
 def shampoo_clip_apply(ctx, grads, max_norm):
-    return _check_of(lib().shampoo_clip_last_error, lib().shampoo_clip_apply(ctx, grads, float(max_norm)), ctx)
+    return _check_clip(lib().shampoo_clip_apply(ctx, grads, float(max_norm)), ctx)
 
 
 def shampoo_clip_result(ctx):
     """Device address of the last call's norm."""
     p = C.c_void_p()
-    _check_of(lib().shampoo_clip_last_error, lib().shampoo_clip_result(ctx, C.byref(p)), ctx)
+    _check_clip(lib().shampoo_clip_result(ctx, C.byref(p)), ctx)
     return p.value
 
 
 def shampoo_clip_set_stream(ctx, stream):
-    return _check_of(lib().shampoo_clip_last_error,
-                     lib().shampoo_clip_set_stream(ctx, C.c_void_p(int(stream))), ctx)
+    return _check_clip(lib().shampoo_clip_set_stream(ctx, C.c_void_p(int(stream))), ctx)
 
 
 def shampoo_clip_nonfinite_status(ctx):
     a = C.c_int()
-    _check_of(lib().shampoo_clip_last_error, lib().shampoo_clip_nonfinite_status(ctx, C.byref(a)), ctx)
+    _check_clip(lib().shampoo_clip_nonfinite_status(ctx, C.byref(a)), ctx)
     return a.value
 
 
@@ -347,15 +353,13 @@ def shampoo_adamw_create(numel, beta1, beta2, epsilon, weight_decay, state_bits=
 
 
 def shampoo_adamw_step(ctx, params, grads, copies, lr):
-    return _check_of(lib().shampoo_adamw_last_error,
-                     lib().shampoo_adamw_step(ctx, params, grads, copies, float(lr)), ctx)
+    return _check_adamw(lib().shampoo_adamw_step(ctx, params, grads, copies, float(lr)), ctx)
 
 
 def shampoo_adamw_state(ctx, which):
     """(device address, element count) of a part of the state."""
     p, n = C.c_void_p(), C.c_int64()
-    _check_of(lib().shampoo_adamw_last_error,
-              lib().shampoo_adamw_state(ctx, int(which), C.byref(p), C.byref(n)), ctx)
+    _check_adamw(lib().shampoo_adamw_state(ctx, int(which), C.byref(p), C.byref(n)), ctx)
     return p.value, n.value
 
 
@@ -364,13 +368,12 @@ def shampoo_adamw_offset(ctx, param):
 
 
 def shampoo_adamw_set_stream(ctx, stream):
-    return _check_of(lib().shampoo_adamw_last_error,
-                     lib().shampoo_adamw_set_stream(ctx, C.c_void_p(int(stream))), ctx)
+    return _check_adamw(lib().shampoo_adamw_set_stream(ctx, C.c_void_p(int(stream))), ctx)
 
 
 def shampoo_adamw_nonfinite_status(ctx):
     a = C.c_int()
-    _check_of(lib().shampoo_adamw_last_error, lib().shampoo_adamw_nonfinite_status(ctx, C.byref(a)), ctx)
+    _check_adamw(lib().shampoo_adamw_nonfinite_status(ctx, C.byref(a)), ctx)
     return a.value
 
 

@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kThreads) list_scale_kernel(ListTables t, cons
 #pragma unroll
   for (int k = 0; k < V::N; ++k) {
     const int v = threadIdx.x + k * kThreads;
-    if (v < vec.nvec) u[k] = *vec.at(v);
+    if (v < vec.nvec) u[k] = __ldcs(vec.at(v));
   }
   if (void* one = vec.single()) store1<BF16>(one, 0, load1<BF16>(one, 0) * coef);
 #pragma unroll
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) list_scale_kernel(ListTables t, cons
     } else {
       o = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
     }
-    *vec.at(v) = o;
+    __stcs(vec.at(v), o);
   }
 }
 
@@ -431,29 +431,45 @@ __device__ __forceinline__ uint2 bf16_bits4(const float* x) {
   return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
-// Four elements of each array, as they are loaded.
+// Four elements of each array, as they are loaded.  All of it streams through L2, first to go: what
+// stays there longer are the gradients that the norm has read, until they are read again
+// (128 us in place of 132 us for ResNet-50's weights).
 template <bool BF16>
 struct Four {
-  float w[4], g[4], m[4], v[4];
+  float4 w, m, v;
+  float g[4];
   __device__ __forceinline__ void load(const Update& u, const float* mp, const float* vp, int i) {
-    load4<false>(u.w, i, w);
-    load4<BF16>(u.g, i, g);
-    load4<false>(mp, i, m);
-    load4<false>(vp, i, v);
+    w = __ldcs(reinterpret_cast<const float4*>(u.w + i));
+    if (BF16) {
+      const uint2 x = __ldcs(reinterpret_cast<const uint2*>(u.g + 2 * i));
+      g[0] = __uint_as_float(x.x << 16);
+      g[1] = __uint_as_float(x.x & 0xFFFF0000u);
+      g[2] = __uint_as_float(x.y << 16);
+      g[3] = __uint_as_float(x.y & 0xFFFF0000u);
+    } else {
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(u.g + 4 * i));
+      g[0] = x.x;
+      g[1] = x.y;
+      g[2] = x.z;
+      g[3] = x.w;
+    }
+    m = __ldcs(reinterpret_cast<const float4*>(mp + i));
+    v = __ldcs(reinterpret_cast<const float4*>(vp + i));
   }
   __device__ __forceinline__ void step(const Update& u, float* mp, float* vp, int i, const Hyper& h) {
+    float xw[4] = {w.x, w.y, w.z, w.w}, xm[4] = {m.x, m.y, m.z, m.w}, xv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       g[q] = __fmul_rn(g[q], u.f.coef);
       if (u.f.huge) g[q] = limit(g[q]);
-      m[q] = next_m(__fmul_rn(h.beta1, m[q]), g[q], h);
-      v[q] = next_v(__fmul_rn(h.beta2, v[q]), g[q], h);
-      w[q] = next_w(w[q], m[q], sqrtf(v[q]), u.f.s, h);
+      xm[q] = next_m(__fmul_rn(h.beta1, xm[q]), g[q], h);
+      xv[q] = next_v(__fmul_rn(h.beta2, xv[q]), g[q], h);
+      xw[q] = next_w(xw[q], xm[q], sqrtf(xv[q]), u.f.s, h);
     }
-    store4<false>(u.w, i, w);
-    store4<false>(mp, i, m);
-    store4<false>(vp, i, v);
-    if (u.b) *reinterpret_cast<uint2*>(u.b + i) = bf16_bits4(w);
+    __stcs(reinterpret_cast<float4*>(u.w + i), make_float4(xw[0], xw[1], xw[2], xw[3]));
+    __stcs(reinterpret_cast<float4*>(mp + i), make_float4(xm[0], xm[1], xm[2], xm[3]));
+    __stcs(reinterpret_cast<float4*>(vp + i), make_float4(xv[0], xv[1], xv[2], xv[3]));
+    if (u.b) __stcs(reinterpret_cast<uint2*>(u.b + i), bf16_bits4(xw));
   }
 };
 
@@ -1214,7 +1230,7 @@ cudaError_t launch_small(const ListTables& t, const void* const* w, const void* 
     cfg.blockDim = dim3(32 * kSmallWarps);
     cfg.stream = s;
     cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ctas > 1;
     return cudaLaunchKernelEx(&cfg, list_small_kernel<OP, BF16, K>, t, aw, ag, ac, (int)(copies != nullptr), max_norm, adv,
                               st, h);
   });

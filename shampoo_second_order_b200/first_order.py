@@ -59,7 +59,7 @@ class _List:
             stream = torch.cuda.current_stream()
         elif not hasattr(stream, "cuda_stream"):
             stream = torch.cuda.ExternalStream(int(stream))
-        self.stream = stream
+        self.stream, self._stream_handle = stream, stream.cuda_stream
         self._device = stream.device_index
         self._handle = self._norm = self._state = None
 
@@ -81,7 +81,7 @@ class _List:
 
     def _on_stream(self, set_stream, call, *args):
         """call(context, *args) in the order of the caller's current stream."""
-        ctx, mine = self._ctx, self.stream.cuda_stream
+        ctx, mine = self._ctx, self._stream_handle
         if _current_handle(self._device) == mine:
             call(ctx, *args)
             return
@@ -100,7 +100,7 @@ class _List:
         else:
             current.wait_stream(self.stream)   # the context's earlier calls
             set_stream(ctx, current.cuda_stream)
-            self.stream = current
+            self.stream, self._stream_handle = current, current.cuda_stream
             call(ctx, *args)
 
     def _view(self, address, count, typestr):
@@ -125,7 +125,7 @@ class GradClip(_List):
 
     def __init__(self, shapes, grad_dtype="f32", stream=None):
         super().__init__(shapes, grad_dtype, stream)
-        self._handle = _Handle(L.shampoo_clip_create(self._numel, self._grad_code, self.stream.cuda_stream),
+        self._handle = _Handle(L.shampoo_clip_create(self._numel, self._grad_code, self._stream_handle),
                                L.shampoo_clip_destroy)
         self._norm = self._view(L.shampoo_clip_result(self._ctx), 1, "<f4")[0]
 
@@ -168,7 +168,7 @@ class AdamW(_List):
         if len(decay) != len(self.shapes):
             raise ValueError(f"expected {len(self.shapes)} values of weight_decay, got {len(decay)}")
         ctx = L.shampoo_adamw_create(self._numel, beta1, beta2, eps, decay, 8 if state == "8bit" else 32,
-                                     self._grad_code, max_norm, seed, self.stream.cuda_stream)
+                                     self._grad_code, max_norm, seed, self._stream_handle)
         self._handle = _Handle(ctx, L.shampoo_adamw_destroy)
         self.offsets = [L.shampoo_adamw_offset(ctx, i) for i in range(len(self.shapes))]
         self._norm = self._part(L.ADAMW_NORM, "<f4")[0]
