@@ -3,7 +3,8 @@
 ``python -m shampoo_second_order_b200.build`` (or ``build()``) writes
 ``libshampoo_b200.so`` next to this file.  Each .cu file is compiled to an
 object in ``_build/`` (in parallel), then linked into one shared library with
-the CUDA runtime linked statically.
+the CUDA runtime linked statically.  Beside it, ``_tensors.so``: a CPython module
+against torch's headers that reads the pointers of a tensor list (``csrc/tensors.cpp``).
 """
 from __future__ import annotations
 
@@ -12,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libshampoo_b200.so")
+TENSORS = os.path.join(HERE, "_tensors.so")
 SOURCES = ["api.cu", "k_stats.cu", "k_roots.cu", "k_apply.cu", "k_tc.cu", "k_tc2.cu", "k_ozaki.cu", "noalloc.cu", "plan.cu",
            "k_adamw.cu", "lists.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -47,10 +50,28 @@ def _compile(src: str, verbose: bool, ptxas_v: bool) -> str:
     return obj
 
 
+def _build_tensors(verbose: bool) -> None:
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = os.path.join(base, "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_path("include"), os.path.join(CSRC, "tensors.cpp"), "-o", TENSORS,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on tensors.cpp:\n{r.stdout}\n{r.stderr}")
+
+
 def build(verbose: bool = False, ptxas_v: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        tensors = ex.submit(_build_tensors, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose, ptxas_v), SOURCES))
+        tensors.result()
     cmd = [nvcc(), *ARCH, "-shared", "-o", LIB, *objs, "-cudart", "static"]
     if verbose:
         print(" ".join(cmd), flush=True)

@@ -8,7 +8,7 @@ namespace shampoo {
 
 constexpr int kListChunk = 8192;   // elements per CTA of the float32 step
 constexpr int kGradChunk = 32768;  // bytes of gradients that a CTA has in flight
-constexpr int kSmallBlocks = 512;  // of the lists that one cluster does
+constexpr int kSmallBlocks = 256;  // of the lists that one cluster does
 constexpr int kSmallCtas = 8;
 constexpr int kListWarps = 8;      // warps per CTA of the list kernels
 constexpr int kQBlock = 256;       // elements per scale of the 8-bit moments; every

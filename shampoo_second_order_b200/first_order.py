@@ -6,14 +6,15 @@ from __future__ import annotations
 import ctypes as C
 from array import array
 from math import prod
-from operator import attrgetter
 
 import torch
-from torch import Tensor
 
 from . import _lib as L
+try:
+    from . import _tensors
+except ImportError as e:
+    raise RuntimeError(f"_tensors.so is not built for this torch ({e}); run python -m shampoo_second_order_b200.build") from e
 
-_dtype = attrgetter("dtype")
 # the handle of a device's current stream, without an object around it
 _current_handle = torch._C._cuda_getCurrentRawStream
 
@@ -50,7 +51,7 @@ class _List:
         if grad_dtype not in ("f32", "bf16"):
             raise ValueError('grad_dtype must be "f32" or "bf16"')
         self.shapes = [tuple(int(d) for d in s) for s in shapes]
-        self._numel = [prod(s) for s in self.shapes]   # checked on every call
+        self._numel = array("q", [prod(s) for s in self.shapes])   # checked on every call
         self.grad_dtype = torch.bfloat16 if grad_dtype == "bf16" else torch.float32
         self._grad_code = L.BF16 if grad_dtype == "bf16" else L.F32
         # without a stream of its own the context follows the caller's current one
@@ -68,16 +69,10 @@ class _List:
         ts, n = list(ts), len(self._numel)
         if len(ts) != n:
             raise ValueError(f"expected {n} {what}, got {len(ts)}")
-        device = self._device
-        if n < 8:   # 1 us a tensor in place of 2.4 us for the first
-            fit = all([t.dtype is dtype and t.is_contiguous() and t.get_device() == device for t in ts]) \
-                and [t.numel() for t in ts] == self._numel
-        else:       # 0.33 us a tensor in place of 0.46 us
-            fit = set(map(_dtype, ts)) == {dtype} and all(map(Tensor.is_contiguous, ts)) \
-                and set(map(Tensor.get_device, ts)) == {device} and list(map(Tensor.numel, ts)) == self._numel
-        if not fit:
-            raise ValueError(f"{what} must be contiguous {dtype} tensors of the given shapes on CUDA device {device}")
-        return (C.c_void_p * n).from_buffer(array("Q", map(Tensor.data_ptr, ts)))
+        out = (C.c_void_p * n)()
+        if not _tensors.pointers(ts, self._numel, dtype.itemsize, self._device, out):
+            raise ValueError(f"{what} must be contiguous {dtype} tensors of the given shapes on CUDA device {self._device}")
+        return out
 
     def _on_stream(self, set_stream, call, *args):
         """call(context, *args) in the order of the caller's current stream."""

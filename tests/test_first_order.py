@@ -104,7 +104,8 @@ def test_oracle_random_bits_look_uniform():
 # --------------------------------------------------------------------------
 @pytest.fixture(scope="module")
 def lib():
-    if not os.path.exists(L.LIB_PATH):
+    from shampoo_second_order_b200 import build as B
+    if not os.path.exists(L.LIB_PATH) or not os.path.exists(B.TENSORS):
         import __graft_entry__
         __graft_entry__.build()
     return L.lib()
@@ -156,16 +157,36 @@ def test_null_contexts_are_refused(lib):
     lib.shampoo_adamw_destroy(None)
 
 
-def test_lists_are_checked_before_the_library():
+def test_lists_are_checked_before_the_library(lib):
+    from array import array
     from shampoo_second_order_b200 import AdamW
     opt = object.__new__(AdamW)
-    opt._numel, opt._device, opt.shapes = [6, 4], 0, [(2, 3), (4,)]
+    opt._numel, opt._device, opt.shapes = array("q", [6, 4]), 0, [(2, 3), (4,)]
     ok = [torch.zeros(2, 3), torch.zeros(4)]
-    for bad, why in ((ok[:1], "expected 2"), ([torch.zeros(2, 3), torch.zeros(5)], "contiguous"),
-                     ([torch.zeros(3, 2).t(), torch.zeros(4)], "contiguous"),
+    for bad, why in ((ok[:1], "expected 2"), ([torch.zeros(2, 3), torch.zeros(5)], "contiguous"), ([1, 2], "contiguous"),
+                     ([torch.zeros(3, 2).t(), torch.zeros(4)], "contiguous"), ([None, ok[1]], "contiguous"),
                      ([torch.zeros(2, 3).bfloat16(), torch.zeros(4)], "contiguous"), (ok, "CUDA device 0")):
         with pytest.raises(ValueError, match=why):
             opt._pointers(bad, "grads", torch.float32)
+
+
+@pytest.mark.gpu
+def test_lists_of_the_wrong_tensors_are_refused(cuda):
+    from shampoo_second_order_b200 import AdamW
+    opt = AdamW([(2, 3), (4,)])
+    z = lambda *s, **k: torch.zeros(*s, device="cuda", **k)   # noqa: E731
+    g = [z(2, 3), z(4)]
+    opt.step([z(6), torch.nn.Parameter(z(4))], tuple(g), 0.1)      # any shape of as many elements
+    for bad in ([z(2, 3), z(5)], [z(3, 2).t(), z(4)], [z(2, 3), z(8)[::2]], [z(2, 3), z(4, dtype=torch.bfloat16)],
+                [z(2, 3), z(4, dtype=torch.float16)], [z(2, 3), z(4, dtype=torch.int32)], [z(2, 3), torch.zeros(4)],
+                [z(2, 3), torch.zeros(4, device="meta")], [z(2, 3), 4], [z(2, 3), z(2, 2).to_sparse()]):
+        for lists in ((bad, g), (g, bad)):
+            with pytest.raises(ValueError, match="contiguous"):
+                opt.step(*lists, 0.1)
+    with pytest.raises(ValueError, match="expected 2"):
+        opt.step(g[:1], g, 0.1)
+    with pytest.raises(ValueError, match="copies"):
+        opt.step(g, g, 0.1, copies=g)
 
 
 # --------------------------------------------------------------------------
