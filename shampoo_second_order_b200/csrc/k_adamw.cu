@@ -24,7 +24,6 @@ namespace shampoo {
 namespace {
 
 constexpr int kThreads = 32 * kListWarps;
-constexpr int kSms = 148;
 constexpr float kGradMax = 0x1p63f;   // an element beyond counts as this: its square would pass the largest float
 
 template <int K>
@@ -880,7 +879,9 @@ __device__ __forceinline__ void read_stage(const Stage<BF16>& s, Loaded<BF16>& x
 // bytes, written among other warps' reads of their sector, took half of the step.)  A warp
 // has its next block on the way to shared memory while it steps one, and waits for no
 // other warp: 823 us for 285M parameters, where 32 warps an SM that load straight into
-// registers take 878 us.
+// registers take 878 us.  In a list too short for that, a warp takes one block of a four (per = 1)
+// and writes its scale's byte: 12 us for 1M parameters (18 us by fours), 16 us for 2M (18 us),
+// 35 us for 8M (32 us).
 //
 // The pointers in wp, gp, cp are those of the tensors less their offset in the flat state, so that
 // a tensor's number is all that a block has to look up.
@@ -888,13 +889,15 @@ template <bool BF16, int K>
 __global__ void __launch_bounds__(kThreads, 3) adamw_8bit_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
                                                                  const __grid_constant__ Pointers<K> gp,
                                                                  const __grid_constant__ Pointers<K> cp, int copies,
-                                                                 int p0, int np, int q0, int nq, AdamwState st,
+                                                                 int p0, int np, int q0, int nq, int per, AdamwState st,
                                                                  const ListStep* step, Hyper h) {
   __shared__ Stage<BF16> stages[kListWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // the fours in the reverse of the norm's order: the gradients that it read last are in L2
-  const int k = blockIdx.x * kListWarps + warp;
+  const int item = blockIdx.x * kListWarps + warp;
+  const int k = per == 4 ? item : item >> 2;
   const int four = q0 + nq - 1 - k;
+  const int j0 = per == 4 ? 0 : item & 3, j1 = j0 + per;
   if (k >= nq) return;
   const auto at = [&](Block& b, int p) {
     b.w = static_cast<float*>(const_cast<void*>(wp.p[p - p0])) + b.flat;
@@ -904,13 +907,13 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_8bit_kernel(ListTables t, c
     b.rq = st.rq + b.flat;
   };
   Block b;
-  b.flat = 4 * (int64_t)four * kQBlock;
+  b.flat = (4 * (int64_t)four + j0) * kQBlock;
   const int p = t.fours[four];
   bool through = false;   // shared memory
   if (p >= 0) {
     at(b, p);
     through = wide<BF16>(b.w, b.g, b.b);
-    if (through) fetch(stages[warp][0], b);
+    if (through) fetch(stages[warp][j0 & 1], b);
   }
   end_fetch();
   wait_for_previous();
@@ -933,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_8bit_kernel(ListTables t, c
   };
   if (through) {
 #pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
+    for (int j = j0; j < j1; ++j) {
       Block next = b;
       next.w += kQBlock;
       next.g += kQBlock * (BF16 ? 2 : 4);
@@ -941,7 +944,7 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_8bit_kernel(ListTables t, c
       next.mq += kQBlock;
       next.rq += kQBlock;
       next.flat += kQBlock;
-      if (j < 3) fetch(stages[warp][(j + 1) & 1], next);
+      if (j + 1 < j1) fetch(stages[warp][(j + 1) & 1], next);
       end_fetch();
       asm volatile("cp.async.wait_group 1;" ::: "memory");   // all but the latest
       __syncwarp();
@@ -956,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_8bit_kernel(ListTables t, c
     }
   } else {
 #pragma unroll 1
-    for (int j = 0; j < 4; ++j) {
+    for (int j = j0; j < j1; ++j) {
       const int64_t blk = 4 * (int64_t)four + j;
       int own = p;
       b.flat = blk * kQBlock;
@@ -975,9 +978,13 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_8bit_kernel(ListTables t, c
       put_scales(j);
     }
   }
-  if (lane == 0) {
+  if (lane != 0) return;
+  if (per == 4) {
     reinterpret_cast<uint32_t*>(st.ms)[four] = ms;
     reinterpret_cast<uint32_t*>(st.rs)[four] = rs;
+  } else {
+    st.ms[4 * (int64_t)four + j0] = (uint8_t)(ms >> (8 * j0));
+    st.rs[4 * (int64_t)four + j0] = (uint8_t)(rs >> (8 * j0));
   }
 }
 
@@ -1293,9 +1300,10 @@ cudaError_t launch_adamw_8bit(const ListTables& t, float* const* w, const void* 
       return a;
     };
     const Pointers<K> aw = less(w, 4), ag = less(g, bf16 ? 2 : 4), ac = copies ? less(copies, 2) : Pointers<K>{};
-    const int ctas = (nq + kListWarps - 1) / kListWarps;
+    const int per = nq < kSms * 3 * kListWarps ? 1 : 4;
+    const int ctas = (nq * (4 / per) + kListWarps - 1) / kListWarps;
     return launch_early(bf16 ? adamw_8bit_kernel<true, K> : adamw_8bit_kernel<false, K>, ctas, s, t, aw, ag, ac,
-                        (int)(copies != nullptr), p0, np, q0, nq, st, step, h);
+                        (int)(copies != nullptr), p0, np, q0, nq, per, st, step, h);
   });
 }
 

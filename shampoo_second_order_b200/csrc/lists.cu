@@ -107,12 +107,17 @@ shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dt
   if (e != cudaSuccess) return cuda_error(l, e, "cudaGetDevice");
   l->numel.assign(numel, numel + nparams);
   std::vector<ListChunk> chunks, gchunks, blocks;
-  const int grad_chunk = kGradChunk / (l->bf16 ? 2 : 4);
+  // chunks are smaller where full ones would leave some of the SMs' four CTAs without any
+  int64_t elements = 0;
+  for (int i = 0; i < nparams; ++i) elements += numel[i];
+  const int64_t share = (elements / (4 * kSms) + 1024) / 1024 * 1024;
+  const int64_t chunk = std::min<int64_t>(kListChunk, share);
+  const int64_t grad_chunk = std::min<int64_t>(kGradChunk / (l->bf16 ? 2 : 4), share);
   for (int i = 0; i < nparams; ++i) {
     if (i % kListGroup == 0) l->groups.push_back(Group{i, 0, (int)chunks.size(), 0, (int)gchunks.size(), 0, 0});
     l->offset.push_back(l->total);
-    for (int64_t s = 0; s < numel[i]; s += kListChunk)
-      chunks.push_back(ListChunk{i, (int)std::min<int64_t>(kListChunk, numel[i] - s), s, l->total + s});
+    for (int64_t s = 0; s < numel[i]; s += chunk)
+      chunks.push_back(ListChunk{i, (int)std::min<int64_t>(chunk, numel[i] - s), s, l->total + s});
     for (int64_t s = 0; s < numel[i]; s += grad_chunk)
       gchunks.push_back(ListChunk{i, (int)std::min<int64_t>(grad_chunk, numel[i] - s), s, l->total + s});
     l->total += (numel[i] + kQBlock - 1) / kQBlock * kQBlock;

@@ -6,6 +6,7 @@
 
 namespace shampoo {
 
+constexpr int kSms = 148;
 constexpr int kListChunk = 8192;   // elements per CTA of the float32 step
 constexpr int kGradChunk = 32768;  // bytes of gradients that a CTA has in flight
 constexpr int kSmallBlocks = 256;  // of the lists that one cluster does
@@ -51,8 +52,8 @@ struct ListAdvance {
 
 // The tables of a pass over the gradients.
 struct ListTables {
-  const ListChunk* chunks;   // of kListChunk elements
-  const ListChunk* gchunks;  // of kGradChunk bytes of gradients
+  const ListChunk* chunks;   // of up to kListChunk elements
+  const ListChunk* gchunks;  // of up to kGradChunk bytes of gradients
   double* partial;        // [ngchunks] sums of squares of runs of a tensor's chunks, with the run's last
   double* csum;           // [nctas] and of all that a CTA of the pass has read
   unsigned* mark;         // [n] the last pass that met an element of it that is not finite
