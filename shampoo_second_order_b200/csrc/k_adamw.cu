@@ -363,9 +363,10 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 struct Hyper {
   float beta1, omb1, beta2, omb2, eps;
   float2 omb1_2, nbeta2_2, nomb2_2, eps_2;   // twice each, as the packed instructions read them; -beta2, -omb2
+  float2 minus_zero_2;
 };
 __host__ Hyper hyper(float beta1, float omb1, float beta2, float omb2, float eps) {
-  return Hyper{beta1, omb1, beta2, omb2, eps, {omb1, omb1}, {-beta2, -beta2}, {-omb2, -omb2}, {eps, eps}};
+  return Hyper{beta1, omb1, beta2, omb2, eps, {omb1, omb1}, {-beta2, -beta2}, {-omb2, -omb2}, {eps, eps}, {-0.0f, -0.0f}};
 }
 
 // What the gradient pass leaves for a tensor.
@@ -718,6 +719,9 @@ __device__ __forceinline__ F2 negative_root(F2 nv) {
 template <class From, class Store>
 __device__ __forceinline__ void step_moments(F2 (&w)[4], F2 (&g)[4], F2 (&m)[4], F2 (&r)[4], int& em, int& er,
                                              const Factors& f, const Hyper& h, uint32_t first, From from, Store store) {
+  // The compiler contracts packed products and sums, as scalar ones of these roundings it would
+  // not: a sum takes its products as products plus a -0 that it does not know.
+  const F2 none = f2(h.minus_zero_2);
   // b1 (code * scale) is (b1 scale) code: the scale is a power of two
   const F2 b1ms = f2(h.beta1 * scale_of(em)), rs = f2(scale_of(er));
 #pragma unroll
@@ -732,9 +736,9 @@ __device__ __forceinline__ void step_moments(F2 (&w)[4], F2 (&g)[4], F2 (&m)[4],
   float mm = 0.0f, vm = 0.0f, ml = FLT_MAX, vl = FLT_MAX;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    m[k] = m[k] * b1ms + f2(h.omb1_2) * g[k];
+    m[k] = fma2(m[k], b1ms, none) + fma2(f2(h.omb1_2), g[k], none);
     r[k] = r[k] * rs;
-    r[k] = f2(h.nbeta2_2) * (r[k] * r[k]) + f2(h.nomb2_2) * g[k] * g[k];   // -v
+    r[k] = fma2(f2(h.nbeta2_2), r[k] * r[k], none) + fma2(f2(h.nomb2_2) * g[k], g[k], none);   // -v
     mm = largest(mm, m[k]);
     ml = smallest(ml, m[k]);
     vm = largest(vm, r[k]);

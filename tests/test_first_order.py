@@ -448,6 +448,53 @@ def test_adamw_clips_gradients_beyond_the_range_of_their_squares(cuda):
     check_step(opt, P, 1e-3, [0.0, 0.0], 1.0, 0, False)
 
 
+def codes_of_f32(x, bits, square):
+    """(e4m3 values, scale bytes) of float32 rows x >= 0 or of any sign, each operation rounded to float32."""
+    e = (((x.abs().amax(1).view(torch.int32) + 0x1FFFFF) >> 23) - 8).clamp(min=1)
+    a = torch.ldexp(x.abs(), (127 - e)[:, None])
+    lift = torch.where(a < 2.0 ** -6, 2.0 ** -6, 0.0)
+    word = (a + lift).view(torch.int32)
+    if square:
+        lo = (word & -0x100000).view(torch.float32) - lift
+        gap = (word & 0x7F800000).view(torch.float32) * 0.125
+        y = torch.where((a - lo) * (a + lo) > bits.float() * 2.0 ** -16 * (gap * (2.0 * lo + gap)), lo + gap, lo)
+    else:
+        y = ((word + (bits.int() << 4)) & -0x100000).view(torch.float32) - lift
+    return torch.copysign(y, x), e
+
+
+@gpu
+@pytest.mark.parametrize("gdt", ["f32", "bf16"])
+@pytest.mark.parametrize("n,shift", [(1 << 22, 0), (1 << 20, 1), (40000, 0), (40000, 3)])
+def test_8bit_codes_are_those_of_operations_rounded_one_by_one(cuda, gdt, n, shift):
+    """Every code equal, with no tolerance: a product fused with its sum changes a last bit in a fifth of the moments, and
+    the code of about one element in a million; two steps on, at both alignments and in both kernels."""
+    from shampoo_second_order_b200 import AdamW
+    gen = torch.Generator("cuda").manual_seed(n + shift)
+    size = torch.exp(2.0 * torch.randn(n, device="cuda", generator=gen)) * 1e-3
+    opt = AdamW([(n,)], B1, B2, EPS, 0.0, "8bit", gdt, seed=12)
+    w = torch.zeros(n + shift, device="cuda")[shift:]
+    b1, omb1, b2, omb2 = (torch.tensor(x, dtype=torch.float32, device="cuda") for x in (B1, 1 - B1, B2, 1 - B2))
+    for t in (1, 2, 3):
+        g = torch.empty(n + shift, device="cuda", dtype=torch.bfloat16 if gdt == "bf16" else torch.float32)[shift:]
+        g.copy_(torch.randn(n, device="cuda", generator=gen) * size)
+        s = {k: x.clone() for k, x in opt.state_tensors().items()}
+        opt.step([w], [g], 1e-3)
+        pad = -n % 256
+        x = torch.nn.functional.pad(g.float(), (0, pad)).view(-1, 256)
+        m0 = s["m"].float().view(-1, 256) * s["m_scale"].float()[:, None]
+        r0 = s["r"].float().view(-1, 256) * s["r_scale"].float()[:, None]
+        m = b1 * m0 + omb1 * x
+        r = (b2 * (r0 * r0) + omb2 * x * x).sqrt()
+        bits = torch.from_numpy(O.random_bits(12, t, 0, n + pad).astype(np.int64)).cuda().view(-1, 256)
+        now = opt.state_tensors()
+        for name, y, b, square in (("m", m, bits & 0xFFFF, False), ("r", r, bits >> 16, True)):
+            want, e = codes_of_f32(y, b, square)
+            assert torch.equal(now[name + "_scale"].view(torch.uint8).int(), e)
+            got = now[name].float().view(-1, 256)
+            assert torch.equal(got, want), ((got != want).sum(), (got != want).nonzero()[:4])
+
+
 @gpu
 def test_8bit_moments_have_no_drift(cuda):
     """Two thousand steps on noise: the mean of v over 2^16 elements follows the one in 32 bits.  The stochastic
