@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <cstring>
 #include <memory>
 #include <new>
 #include <string>
@@ -39,7 +40,7 @@ struct List {
   int64_t total = 0;   // elements of the flat state, the gaps between tensors included
   std::vector<Group> groups;
   ListTables tab{};
-  std::vector<void*> allocs;
+  void* memory = nullptr;
   std::string err;
 };
 
@@ -65,24 +66,53 @@ shampoo_status cuda_error(List* l, cudaError_t e, const char* what) {
   return refuse(l, SHAMPOO_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
-// Zeroed device memory, freed with the list.
-template <class T>
-cudaError_t zeroed(List* l, T** p, int64_t count) {
-  void* q = nullptr;
-  cudaError_t e = cudaMalloc(&q, (size_t)count * sizeof(T));
+// The list's device memory: one allocation, the tables in front, zeros behind.
+struct Layout {
+  std::vector<char> image;   // the tables
+  size_t zeros = 0;          // bytes behind them
+  struct Part {
+    void** p;
+    size_t at;
+    bool zero;
+  };
+  std::vector<Part> parts;
+
+  static size_t up(size_t n) { return (n + 255) & ~size_t(255); }
+  template <class T>
+  void table(const T** p, const std::vector<T>& v) {
+    parts.push_back(Part{reinterpret_cast<void**>(const_cast<T**>(p)), image.size(), false});
+    image.resize(image.size() + up(v.size() * sizeof(T)));
+    std::memcpy(image.data() + parts.back().at, v.data(), v.size() * sizeof(T));
+  }
+  template <class T>
+  void room(T** p, int64_t count) {
+    parts.push_back(Part{reinterpret_cast<void**>(p), zeros, true});
+    zeros += up((size_t)count * sizeof(T));
+  }
+};
+
+// Allocates the layout and fills it; waits for the stream.
+shampoo_status allocate(List* l, const Layout& y) {
+  const size_t tables = y.image.size();
+  cudaError_t e = cudaMalloc(&l->memory, tables + y.zeros);
   if (e != cudaSuccess) {
     cudaGetLastError();   // reported here; no later launch should find it
-    return e;
+    return refuse(l, SHAMPOO_ENOMEM, std::string("device allocation failed: ") + cudaGetErrorString(e));
   }
-  l->allocs.push_back(q);
-  *p = static_cast<T*>(q);
-  return cudaMemsetAsync(q, 0, (size_t)count * sizeof(T), l->stream);
+  char* base = static_cast<char*>(l->memory);
+  for (const Layout::Part& x : y.parts) *x.p = base + x.at + (x.zero ? tables : 0);
+  // pageable source: staged by the driver before the call returns
+  e = cudaMemcpyAsync(base, y.image.data(), tables, cudaMemcpyHostToDevice, l->stream);
+  if (e == cudaSuccess && y.zeros) e = cudaMemsetAsync(base + tables, 0, y.zeros, l->stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(l->stream);
+  return e == cudaSuccess ? SHAMPOO_OK : cuda_error(l, e, "set-up");
 }
 
 void release(List* l) {
+  if (!l->memory) return;
   OnDevice on(l->device);
-  if (!l->allocs.empty()) cudaStreamSynchronize(l->stream);
-  for (void* q : l->allocs) cudaFree(q);
+  cudaStreamSynchronize(l->stream);
+  cudaFree(l->memory);
 }
 
 // Checks the list's sizes, then its tables on the host and the device.  The
@@ -100,7 +130,8 @@ shampoo_status check_list(int nparams, const int64_t* numel, int grad_dtype) {
   return SHAMPOO_OK;
 }
 
-shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dtype, void* stream) {
+// The list's tables and the work space of its passes.
+shampoo_status make_list(List* l, Layout* y, int nparams, const int64_t* numel, int grad_dtype, void* stream) {
   l->stream = static_cast<cudaStream_t>(stream);
   l->bf16 = grad_dtype == SHAMPOO_BF16;
   cudaError_t e = cudaGetDevice(&l->device);
@@ -135,34 +166,23 @@ shampoo_status make_list(List* l, int nparams, const int64_t* numel, int grad_dt
   l->tab.nchunks = (int)chunks.size();
   l->tab.ngchunks = (int)gchunks.size();
   l->tab.nparams = nparams;
-  ListChunk *d = nullptr, *dg = nullptr, *db = nullptr;
   for (Group& g : l->groups) {
     g.b0 = l->tab.nctas;
     l->tab.nctas += list_norm_ctas(g.ng);
   }
-  if ((e = zeroed(l, &d, l->tab.nchunks)) != cudaSuccess || (e = zeroed(l, &dg, l->tab.ngchunks)) != cudaSuccess ||
-      (!blocks.empty() && (e = zeroed(l, &db, l->tab.nblocks)) != cudaSuccess) || (e = zeroed(l, &l->tab.partial, l->tab.ngchunks)) != cudaSuccess ||
-      (e = zeroed(l, &l->tab.csum, l->tab.nctas)) != cudaSuccess ||
-      (e = zeroed(l, &l->tab.mark, nparams)) != cudaSuccess || (e = zeroed(l, &l->tab.skip, nparams)) != cudaSuccess || (e = zeroed(l, &l->tab.result, 1)) != cudaSuccess)
-    return refuse(l, SHAMPOO_ENOMEM, std::string("device allocation failed: ") + cudaGetErrorString(e));
-  l->tab.chunks = d;
-  l->tab.gchunks = dg;
-  l->tab.blocks = db;
-  // pageable sources: staged by the driver before the calls return
-  const ListResult first{0.f, 1.f, 0, 0, 1, 0};
-  e = cudaMemcpyAsync(l->tab.result, &first, sizeof(first), cudaMemcpyHostToDevice, l->stream);
-  if (e == cudaSuccess)
-    e = cudaMemcpyAsync(d, chunks.data(), chunks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
-  if (e == cudaSuccess)
-    e = cudaMemcpyAsync(dg, gchunks.data(), gchunks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
-  if (e == cudaSuccess && db)
-    e = cudaMemcpyAsync(db, blocks.data(), blocks.size() * sizeof(ListChunk), cudaMemcpyHostToDevice, l->stream);
-  if (e != cudaSuccess) return cuda_error(l, e, "upload of the chunk table");
+  y->table(&l->tab.chunks, chunks);
+  y->table(&l->tab.gchunks, gchunks);
+  if (!blocks.empty()) y->table(&l->tab.blocks, blocks);
+  y->table(const_cast<const ListResult**>(&l->tab.result), std::vector<ListResult>{{0.f, 1.f, 0, 0, 1, 0}});
+  y->room(&l->tab.partial, l->tab.ngchunks);
+  y->room(&l->tab.csum, l->tab.nctas);
+  y->room(&l->tab.mark, nparams);
+  y->room(&l->tab.skip, nparams);
   return SHAMPOO_OK;
 }
 
 // The tables of the 8-bit step: which tensor each block of the flat state belongs to.
-shampoo_status make_blocks(List* l) {
+void make_blocks(List* l, Layout* y) {
   const int n = (int)l->numel.size();
   const int64_t blocks = l->total / kQBlock;
   std::vector<int> owner(blocks), fours((blocks + 3) / 4);
@@ -176,21 +196,10 @@ shampoo_status make_blocks(List* l) {
     const int p = owner[4 * q];
     fours[q] = (4 * q + 4) * kQBlock <= ends[p] ? p : -1;
   }
-  int *d_owner = nullptr, *d_fours = nullptr;
-  int64_t* d_ends = nullptr;
-  cudaError_t e = zeroed(l, &d_owner, blocks);
-  if (e == cudaSuccess) e = zeroed(l, &d_fours, (int64_t)fours.size());
-  if (e == cudaSuccess) e = zeroed(l, &d_ends, n);
-  if (e != cudaSuccess) return refuse(l, SHAMPOO_ENOMEM, std::string("device allocation failed: ") + cudaGetErrorString(e));
-  e = cudaMemcpyAsync(d_owner, owner.data(), owner.size() * sizeof(int), cudaMemcpyHostToDevice, l->stream);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(d_fours, fours.data(), fours.size() * sizeof(int), cudaMemcpyHostToDevice, l->stream);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(d_ends, ends.data(), n * sizeof(int64_t), cudaMemcpyHostToDevice, l->stream);
-  if (e != cudaSuccess) return cuda_error(l, e, "upload of the block tables");
-  l->tab.owner = d_owner;
-  l->tab.fours = d_fours;
-  l->tab.ends = d_ends;
+  y->table(&l->tab.owner, owner);
+  y->table(&l->tab.fours, fours);
+  y->table(&l->tab.ends, ends);
   l->tab.nqblocks = blocks;
-  return SHAMPOO_OK;
 }
 
 // One pointer list of a call: what it is called, its element size, whether the call writes to it.
@@ -292,11 +301,9 @@ shampoo_status shampoo_clip_create(shampoo_clip** out, int nparams, const int64_
     shampoo_status st = check_list(nparams, numel, grad_dtype);
     if (st != SHAMPOO_OK) return st;
     std::unique_ptr<shampoo_clip, void (*)(shampoo_clip*)> c(new shampoo_clip(), shampoo_clip_destroy);
-    st = make_list(&c->list, nparams, numel, grad_dtype, cuda_stream);
-    if (st == SHAMPOO_OK) {
-      const cudaError_t e = cudaStreamSynchronize(c->list.stream);
-      if (e != cudaSuccess) st = cuda_error(&c->list, e, "set-up");
-    }
+    Layout y;
+    st = make_list(&c->list, &y, nparams, numel, grad_dtype, cuda_stream);
+    if (st == SHAMPOO_OK) st = allocate(&c->list, y);
     if (st != SHAMPOO_OK) {
       set_global_error(c->list.err);
       return st;
@@ -409,30 +416,25 @@ shampoo_status shampoo_adamw_create(shampoo_adamw** out, int nparams, const int6
     a->eps = epsilon;
     a->max_norm = max_norm;
     a->seed = (uint64_t)seed;
-    st = make_list(l, nparams, numel, grad_dtype, cuda_stream);
+    Layout y;
+    st = make_list(l, &y, nparams, numel, grad_dtype, cuda_stream);
     if (st == SHAMPOO_OK) {
-      cudaError_t e = zeroed(l, &a->step, nparams);
-      if (e == cudaSuccess) e = zeroed(l, &a->factors, nparams);
-      if (e == cudaSuccess) e = zeroed(l, &a->decay, nparams);
+      y.table(const_cast<const double**>(&a->decay), weight_decay ? std::vector<double>(weight_decay, weight_decay + nparams)
+                                                                  : std::vector<double>(nparams, 0.0));
+      y.room(&a->step, nparams);
+      y.room(&a->factors, nparams);
       if (state_bits == 32) {
-        if (e == cudaSuccess) e = zeroed(l, &a->st.m, l->total);
-        if (e == cudaSuccess) e = zeroed(l, &a->st.v, l->total);
+        y.room(&a->st.m, l->total);
+        y.room(&a->st.v, l->total);
       } else {
-        if (e == cudaSuccess) e = zeroed(l, &a->st.mq, l->total);
-        if (e == cudaSuccess) e = zeroed(l, &a->st.rq, l->total);
+        if (l->total > (int64_t)kSmallBlocks * kQBlock) make_blocks(l, &y);
         const int64_t words = (l->total / kQBlock + 3) / 4;   // read and written by the word
-        if (e == cudaSuccess) e = zeroed(l, &a->st.ms, 4 * words);
-        if (e == cudaSuccess) e = zeroed(l, &a->st.rs, 4 * words);
+        y.room(&a->st.mq, l->total);
+        y.room(&a->st.rq, l->total);
+        y.room(&a->st.ms, 4 * words);
+        y.room(&a->st.rs, 4 * words);
       }
-      if (e != cudaSuccess) st = refuse(l, SHAMPOO_ENOMEM, std::string("device allocation failed: ") + cudaGetErrorString(e));
-      else if (state_bits == 8 && !l->tab.blocks) st = make_blocks(l);
-    }
-    if (st == SHAMPOO_OK) {
-      cudaError_t e = cudaSuccess;
-      if (weight_decay)
-        e = cudaMemcpyAsync(a->decay, weight_decay, nparams * sizeof(double), cudaMemcpyHostToDevice, l->stream);
-      if (e == cudaSuccess) e = cudaStreamSynchronize(l->stream);
-      if (e != cudaSuccess) st = cuda_error(l, e, "set-up");
+      st = allocate(l, y);
     }
     if (st != SHAMPOO_OK) {
       set_global_error(l->err);

@@ -120,8 +120,9 @@ class GradClip(_List):
 
     def __init__(self, shapes, grad_dtype="f32", stream=None):
         super().__init__(shapes, grad_dtype, stream)
-        self._handle = _Handle(L.shampoo_clip_create(self._numel, self._grad_code, self._stream_handle),
-                               L.shampoo_clip_destroy)
+        with torch.cuda.device(self._device):
+            ctx = L.shampoo_clip_create(self._numel, self._grad_code, self._stream_handle)
+        self._handle = _Handle(ctx, L.shampoo_clip_destroy)
         self._norm = self._view(L.shampoo_clip_result(self._ctx), 1, "<f4")[0]
 
     def norm(self, grads):
@@ -162,8 +163,9 @@ class AdamW(_List):
         decay = list(weight_decay) if hasattr(weight_decay, "__len__") else [weight_decay] * len(self.shapes)
         if len(decay) != len(self.shapes):
             raise ValueError(f"expected {len(self.shapes)} values of weight_decay, got {len(decay)}")
-        ctx = L.shampoo_adamw_create(self._numel, beta1, beta2, eps, decay, 8 if state == "8bit" else 32,
-                                     self._grad_code, max_norm, seed, self._stream_handle)
+        with torch.cuda.device(self._device):
+            ctx = L.shampoo_adamw_create(self._numel, beta1, beta2, eps, decay, 8 if state == "8bit" else 32,
+                                         self._grad_code, max_norm, seed, self._stream_handle)
         self._handle = _Handle(ctx, L.shampoo_adamw_destroy)
         self.offsets = [L.shampoo_adamw_offset(ctx, i) for i in range(len(self.shapes))]
         self._norm = self._part(L.ADAMW_NORM, "<f4")[0]
