@@ -31,8 +31,10 @@ struct Pointers {
   const void* p[K];
 };
 
-// The kernels after the gradient pass start while it runs: they fetch what does not
-// depend on it, then wait for its end.
+// Every kernel here may be launched before the one in front of it in the stream has ended (2 us less
+// a call), and waits for that end before it reads what that one may write.  The kernels
+// after the gradient pass start while it runs, and first fetch what does not depend on it: the
+// pass itself has waited for all that came before.
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
@@ -210,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 4) list_norm_kernel(ListTables t, co
   using V = Vectors<BF16>;
   __shared__ double red[kListWarps];
   __shared__ bool last;
+  wait_for_previous();
   let_next_start();
   const unsigned pass = t.result->pass;
   const int i0 = c0 + (int)((int64_t)nc * blockIdx.x / gridDim.x);
@@ -1086,12 +1089,13 @@ __global__ void __launch_bounds__(32 * kSmallWarps)
   __shared__ int bads[kSmallWarps], all_bad[2][kSmallCtas], skipped;
   const int lane = threadIdx.x & 31, warps = gridDim.x * kSmallWarps;
   const int b0 = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;
-  const unsigned pass = __ldcg(&t.result->pass);
   const auto gradient = [&](const ListChunk& c) {
     return static_cast<const char*>(gp.p[c.param]) + c.start * (BF16 ? 2 : 4);
   };
+  wait_for_previous();
   // shared memory of another CTA may be written once that has started: waited for in cluster_total
   asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+  const unsigned pass = __ldcg(&t.result->pass);
   if (threadIdx.x == 0) skipped = 0;
   double sum = 0.0;
   bool bad = false;
@@ -1224,9 +1228,8 @@ cudaError_t launch_list_norm(const ListTables& t, const void* const* g, int p0, 
     constexpr int K = decltype(n)::value;
     const Pointers<K> a = pack<K>(g + p0, np);
     const int ctas = list_norm_ctas(nc);
-    if (bf16) list_norm_kernel<true, K><<<ctas, kThreads, 0, s>>>(t, a, p0, np, c0, nc, b0, max_norm, adv);
-    else list_norm_kernel<false, K><<<ctas, kThreads, 0, s>>>(t, a, p0, np, c0, nc, b0, max_norm, adv);
-    return cudaGetLastError();
+    return launch_early(bf16 ? list_norm_kernel<true, K> : list_norm_kernel<false, K>, ctas, s, t, a, p0, np, c0, nc, b0,
+                        max_norm, adv);
   });
 }
 
@@ -1248,16 +1251,18 @@ cudaError_t launch_small(const ListTables& t, const void* const* w, const void* 
     const Pointers<K> ag = pack<K>(g, t.nparams);
     const Pointers<K> ac = copies ? pack<K>(copies, t.nparams) : Pointers<K>{};
     const int ctas = list_small_ctas(t.nblocks);
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = ctas;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(32 * kSmallWarps);
     cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = ctas > 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, list_small_kernel<OP, BF16, K>, t, aw, ag, ac, (int)(copies != nullptr), max_norm, adv,
                               st, h);
   });

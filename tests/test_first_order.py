@@ -744,3 +744,12 @@ def test_shampoo_and_adamw_share_a_clipped_step(cuda, state):
             want, _, _ = O.adamw(w_before[2 + i], g[2 + i].astype(np.float64).ravel() / 3, m0, v0, t + 1, lr, B1, B2, EPS, 0.01)
             assert (np.abs(f64(W[2 + i]) - want) <= 1.01 * (2 * U * np.abs(want) + 100 * U * lr * 3.2)).all()
     sh.close()
+
+
+@gpu
+@pytest.mark.parametrize("args,says", [(["--optimizer", "adamw"], "adamw"), (["--optimizer", "adamw8", "--max-norm", "0.5"], "adamw8"),
+                                       (["--max-norm", "0.5"], "pair tiles")])
+def test_run_steps_command(cuda, capsys, args, says):
+    from shampoo_second_order_b200 import run_steps
+    assert run_steps.main(["--config", "transformer_layer_b512", "--params", "2", "--steps", "2"] + args) == 0
+    assert f"({says})" in capsys.readouterr().out
