@@ -6,7 +6,12 @@
 //   t <- t + 1;  m <- b1 m + (1 - b1) g;  v <- b2 v + (1 - b2) g^2
 //   w <- w (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 //
-// All of it is bound by HBM: a few operations an element against 10 to 34 bytes.
+// Large lists are bound by HBM: a few operations an element against 10 to 34 bytes (with 8-bit
+// moments 65 instructions, which take nearly as long), and the gradients are read twice, since no
+// weight may move before the norm and the tensors to skip are known.  On a B200 (6.47 TB/s measured
+// copy): 285M parameters in float32 1350 us (8.0 GB read and written once, 1.1 GB read again: 1411 us at
+// that rate), with 8-bit moments, bfloat16 gradients and copies 785 us (5.1 GB: 794 us), clipping as many
+// bfloat16 gradients 245 us (1.7 GB: 265 us).  Small lists are bound by their launch: 4 to 6 us.
 #include <float.h>
 
 #include <algorithm>
@@ -68,19 +73,6 @@ template <bool BF16>
 __device__ __forceinline__ void store1(void* p, int64_t i, float x) {
   if (BF16) reinterpret_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
   else reinterpret_cast<float*>(p)[i] = x;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void store4(void* p, int64_t i, const float (&x)[4]) {
-  if (BF16) {
-    __nv_bfloat162 lo = __floats2bfloat162_rn(x[0], x[1]), hi = __floats2bfloat162_rn(x[2], x[3]);
-    uint2 u;
-    u.x = *reinterpret_cast<uint32_t*>(&lo);
-    u.y = *reinterpret_cast<uint32_t*>(&hi);
-    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p) + i) = u;
-  } else {
-    *reinterpret_cast<float4*>(reinterpret_cast<float*>(p) + i) = make_float4(x[0], x[1], x[2], x[3]);
-  }
 }
 
 // Chunks start at multiples of kQBlock, so the tensor's own address decides.
@@ -326,7 +318,7 @@ __global__ void __launch_bounds__(kThreads) list_scale_kernel(ListTables t, cons
 
 // ---------------- AdamW ----------------
 
-// Two floats that the packed instructions of sm_100 work on, each rounded as alone.
+// Two floats that the packed instructions of sm_100 work on.
 struct F2 {
   unsigned long long v;
 };
@@ -436,7 +428,7 @@ __device__ __forceinline__ uint2 bf16_bits4(const float* x) {
 
 // Four elements of each array, as they are loaded.  All of it streams through L2, first to go: what
 // stays there longer are the gradients that the norm has read, until they are read again
-// (128 us in place of 132 us for ResNet-50's weights).
+// (3 % less time for ResNet-50's weights).
 template <bool BF16>
 struct Four {
   float4 w, m, v;
@@ -497,7 +489,7 @@ __device__ __forceinline__ void step_run(Update& u, float* mp, float* vp, int th
     if (i + 3 * stride < whole) b.load(u, mp, vp, i + 3 * stride);
   }
   // eight loads of each array before the first store, which may be to any of them for all
-  // that the compiler knows: 185 us in place of 110 us for 20M parameters without them
+  // that the compiler knows: 110 us in place of 185 us for 20M parameters without gaps
   for (int o = whole + thread; o < u.c.len; o += 8 * threads) {
     float w[8], g[8], m[8], v[8];
 #pragma unroll
@@ -669,6 +661,11 @@ __device__ __forceinline__ uint2 ld8(const void* p) {
   return o;
 }
 
+// A value that all lanes of a warp have, so that the compiler knows it: addresses and constants
+// then go to uniform registers, which leaves room for a fourth CTA an SM (together 785 us in place of
+// 836 us for 285M parameters).
+__device__ __forceinline__ int same(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // One block of one tensor, where its arrays are.
 struct Block {
   float* w;
@@ -764,8 +761,8 @@ __device__ __forceinline__ void step_moments(F2 (&w)[4], F2 (&g)[4], F2 (&m)[4],
   }
   store();
   // magnitudes order as their bits do, and roots as their squares
-  em = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(mm)));
-  er = root_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(vm)));
+  em = same(scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(mm))));
+  er = same(root_scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(vm))));
   const float im = inverse_scale(em), ir = inverse_scale(er);
   // an element 2^15 below the block's largest: hardly ever, but for zeros
   if (__any_sync(0xffffffffu, ml * im < 0x1p-6f || vl * ir * ir < 0x1.1p-12f)) round_block<true>(m, r, im, -ir, first, from);
@@ -901,21 +898,20 @@ __device__ __forceinline__ void read_stage(const Stage<BF16>& s, Loaded<BF16>& x
 // The blocks of the flat state go to the warps in fours, the scales of which are one word.  (Single
 // bytes, written among other warps' reads of their sector, took half of the step.)  A warp
 // has its next block on the way to shared memory while it steps one, and waits for no
-// other warp: 823 us for 285M parameters, where 32 warps an SM that load straight into
-// registers take 878 us.  In a list too short for that, a warp takes one block of a four (per = 1)
-// and writes its scale's byte: 12 us for 1M parameters (18 us by fours), 16 us for 2M (18 us),
-// 35 us for 8M (32 us).
+// other warp: 6 % less time than loading straight into registers, for 285M parameters.  In a list too
+// short for that, a warp takes one block of a four (per = 1) and writes its scale's byte: with 1M
+// parameters a third less time, with 2M a tenth, with 8M a tenth more.
 //
 // The pointers in wp, gp, cp are those of the tensors less their offset in the flat state, so that
 // a tensor's number is all that a block has to look up.
 template <bool BF16, int K>
-__global__ void __launch_bounds__(kThreads, 3) adamw_8bit_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
+__global__ void __launch_bounds__(kThreads, 4) adamw_8bit_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
                                                                  const __grid_constant__ Pointers<K> gp,
                                                                  const __grid_constant__ Pointers<K> cp, int copies,
                                                                  int p0, int np, int q0, int nq, int per, AdamwState st,
                                                                  const ListStep* step, Hyper h) {
   __shared__ Stage<BF16> stages[kListWarps][2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = same(threadIdx.x >> 5);
   // the fours in the reverse of the norm's order: the gradients that it read last are in L2
   const int item = blockIdx.x * kListWarps + warp;
   const int k = per == 4 ? item : item >> 2;
@@ -931,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_8bit_kernel(ListTables t, c
   };
   Block b;
   b.flat = (4 * (int64_t)four + j0) * kQBlock;
-  const int p = t.fours[four];
+  const int p = same(t.fours[four]);
   bool through = false;   // shared memory
   if (p >= 0) {
     at(b, p);
@@ -1015,7 +1011,8 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_8bit_kernel(ListTables t, c
 //
 // A list of at most kSmallBlocks blocks is done by one launch of one cluster, a
 // warp a block: the CTAs exchange their sums through each other's shared memory.  The
-// two launches take 8 to 10 us for a 64 x 32 tensor, most of it in starting and ending.
+// two launches take 8 to 10 us for a 64 x 32 tensor, this one 4 to 6 us, most of it in starting and
+// ending; from twice as many blocks on the two are faster.
 
 enum : int { kOpNorm, kOpClip, kOpF32, kOp8Bit };
 constexpr int kSmallWarps = 16;
