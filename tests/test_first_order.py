@@ -678,33 +678,50 @@ def test_adamw_state_is_saved_and_restored(cuda, state):
 
 
 @gpu
-def test_adamw_beyond_32_bit_offsets(cuda):
-    """One tensor of 2^31 + 5000 elements with 8-bit moments: what lies behind 2^31 steps as the oracle says."""
-    from shampoo_second_order_b200 import AdamW
-    n, tail = (1 << 31) + 5000, 20000
-    if torch.cuda.mem_get_info()[0] < 40 << 30:
-        pytest.skip("needs 40 GB of device memory")
-    w = torch.zeros(n, device="cuda")
-    g = torch.zeros(n, device="cuda", dtype=torch.bfloat16)
-    x = torch.randn(tail, device="cuda", generator=torch.Generator("cuda").manual_seed(1))
+@pytest.mark.parametrize("state", ["f32", "8bit"])
+def test_adamw_beyond_32_bit_offsets(cuda, state):
+    """Two tensors, the first of 5000 elements more than 2^31, or 2^32 with 8-bit moments: what lies behind that in the first,
+    and the second, whose moments begin there, step as the oracle says; the clipping reaches them too."""
+    from shampoo_second_order_b200 import AdamW, GradClip
+    n, tail, small = (1 << (31 if state == "f32" else 32)) + 5000, 20000, 700
+    if torch.cuda.mem_get_info()[0] < 50 << 30:
+        pytest.skip("needs 50 GB of device memory")
+    gen = torch.Generator("cuda").manual_seed(1)
+    w, w2 = torch.zeros(n, device="cuda"), torch.randn(small, device="cuda", generator=gen) * 0.02
+    g, g2 = torch.zeros(n, device="cuda", dtype=torch.bfloat16), (torch.randn(small, device="cuda", generator=gen) * 1e-3).bfloat16()
+    x = torch.randn(tail, device="cuda", generator=gen)
     w[-tail:] = x * 0.02
     g[-tail:] = (x.flip(0) * 1e-3).bfloat16()
-    opt = AdamW([(n,)], B1, B2, EPS, 0.1, "8bit", "bf16", seed=3)
-    w0, g0 = f64(w[-tail:]), f64(g[-tail:])
-    opt.step([w], [g], 1e-2)
-    want, m, v = O.adamw(w0, g0, np.zeros(tail), np.zeros(tail), 1, 1e-2, B1, B2, EPS, 0.1)
-    assert (np.abs(f64(w[-tail:]) - want) <= 40 * U * (np.abs(w0) + 1e-2)).all()
+    opt = AdamW([(n,), (small,)], B1, B2, EPS, 0.1, state, "bf16", seed=3)
+    assert opt.offsets == [0, (n + 255) // 256 * 256]
+    cases = [(f64(w[-tail:]), f64(g[-tail:]), w[-tail:], n - tail), (f64(w2), f64(g2), w2, opt.offsets[1])]
+    opt.step([w, w2], [g, g2], 1e-2)
+    norm, _ = O.global_norm([f64(g[-tail:]), f64(g2)])
+    assert abs(float(opt.grad_norm()) - norm) <= 10 * U * 1.01 * norm
     assert not w[:-tail].any()
-    # the first whole block from 2^31 on
-    at = 1 << 31
     s = opt.state_tensors()
-    for name, x, square in (("m", m, False), ("r", np.sqrt(v), True)):
-        rows = O.rows(x[at - (n - tail):at - (n - tail) + 2560])
-        e = s[name + "_scale"].view(torch.uint8)[at // 256:at // 256 + 10].cpu().numpy().astype(int)
-        codes = O.e4m3_values()[s[name].view(torch.uint8)[at:at + 2560].cpu().numpy()].reshape(-1, 256)
-        bits = O.random_bits(3, 1, at, 2560).reshape(-1, 256)
-        bits = (bits >> np.uint64(16) if square else bits & np.uint64(0xFFFF)).astype(np.float64)
-        check_codes(rows, 30 * U * np.abs(rows), codes, e, bits, square)
+    for w0, g0, now, first in cases:
+        want, m, v = O.adamw(w0, g0, np.zeros(len(w0)), np.zeros(len(w0)), 1, 1e-2, B1, B2, EPS, 0.1)
+        assert (np.abs(f64(now) - want) <= 40 * U * (np.abs(w0) + 1e-2)).all()
+        at = -(-first // 256) * 256          # whole blocks from here on
+        k = (len(m) - (at - first)) // 256 * 256
+        m, v = m[at - first:][:k], v[at - first:][:k]
+        if state == "f32":
+            assert (np.abs(f64(s["m"][at:at + k]) - m) <= 6 * U * np.abs(m)).all()
+            assert (np.abs(f64(s["v"][at:at + k]) - v) <= 6 * U * v).all()
+            continue
+        for name, x, square in (("m", m, False), ("r", np.sqrt(v), True)):
+            e = s[name + "_scale"].view(torch.uint8)[at // 256:(at + k) // 256].cpu().numpy().astype(int)
+            codes = O.e4m3_values()[s[name].view(torch.uint8)[at:at + k].cpu().numpy()].reshape(-1, 256)
+            bits = O.random_bits(3, 1, at, k).reshape(-1, 256)
+            bits = (bits >> np.uint64(16) if square else bits & np.uint64(0xFFFF)).astype(np.float64)
+            check_codes(O.rows(x), 30 * U * np.abs(O.rows(x)), codes, e, bits, square)
+    del opt, s, w
+    torch.cuda.empty_cache()
+    clip = GradClip([(n,), (small,)], "bf16")
+    assert abs(float(clip.clip([g, g2], norm / 2)) - norm) <= 10 * U * 1.01 * norm
+    for now, was in ((g[-tail:], cases[0][1]), (g2, cases[1][1])):
+        assert (np.abs(f64(now) - was / 2) <= 1.01 * (10 * U + 2.0 ** -8) * np.abs(was) / 2).all()
 
 
 @gpu
