@@ -284,8 +284,8 @@ __global__ void __launch_bounds__(kThreads) list_scale_kernel(ListTables t, cons
   const ListChunk c = t.gchunks[c0 + gridDim.x - 1 - blockIdx.x];
   const V vec(ptr.p[c.param - p0], c.start, c.len);
   wait_for_previous();
-  const float coef = t.result->coef;
-  if (coef == 1.0f || t.skip[c.param]) return;
+  const float coef = __ldcg(&t.result->coef);
+  if (coef == 1.0f || __ldcg(&t.skip[c.param])) return;
   uint4 u[V::N];
 #pragma unroll
   for (int k = 0; k < V::N; ++k) {
@@ -393,13 +393,24 @@ __device__ __forceinline__ void update_of(Update& u, const ListTables& t, const 
   u.aligned = aligned4<false>(u.w) && aligned4<BF16>(u.g) && aligned4<true>(u.b);
 }
 
+// Past L1, which a kernel that starts early may share with the pass that writes them.
+__device__ __forceinline__ ListStep step_of(const ListStep* step, int p) {
+  const float4 s = __ldcg(reinterpret_cast<const float4*>(step + p));
+  return ListStep{s.x, s.y, s.z, __float_as_uint(s.w)};
+}
+__device__ __forceinline__ Factors factors_of(const ListTables& t, const ListStep* step, int p) {
+  Factors f;
+  if (p >= 0) f.s = step_of(step, p);
+  f.coef = __ldcg(&t.result->coef);
+  f.huge = !(__ldcg(&t.result->norm) * f.coef < kGradMax);   // no element exceeds the norm
+  return f;
+}
+
 // Waits for the gradient pass; false where the tensor is skipped.
 __device__ __forceinline__ bool pass_results(Update& u, const ListTables& t, const ListStep* step) {
   wait_for_previous();
-  const int skip = t.skip[u.c.param];
-  u.f.s = step[u.c.param];
-  u.f.coef = t.result->coef;
-  u.f.huge = !(t.result->norm * u.f.coef < kGradMax);   // no element exceeds the norm
+  const int skip = __ldcg(&t.skip[u.c.param]);
+  u.f = factors_of(t, step, u.c.param);
   return !skip;
 }
 
@@ -518,8 +529,10 @@ __device__ __forceinline__ void step_run(Update& u, float* mp, float* vp, int th
   }
 }
 
+// CTAs an SM: 65 us with four, 68 us with three for 12.6M parameters with bfloat16 gradients; 1364 us with
+// four, 1352 us with three for 285M with float32 ones.
 template <bool BF16, int K>
-__global__ void __launch_bounds__(kThreads) adamw_f32_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
+__global__ void __launch_bounds__(kThreads, BF16 ? 4 : 3) adamw_f32_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
                                                              const __grid_constant__ Pointers<K> gp,
                                                              const __grid_constant__ Pointers<K> cp, int copies,
                                                              int p0, int c0, AdamwState st,
@@ -680,7 +693,7 @@ struct Block {
 // 32 q + l is lane l's q-th, so that accesses of single elements are those of
 // neighbouring lanes to neighbouring addresses.
 template <bool BF16>
-__device__ __forceinline__ bool wide(const void* w, const void* g, const void* b) {
+__host__ __device__ __forceinline__ bool wide(const void* w, const void* g, const void* b) {
   return ((reinterpret_cast<uintptr_t>(w) & 31) | (reinterpret_cast<uintptr_t>(g) & (BF16 ? 15 : 31)) |
           (reinterpret_cast<uintptr_t>(b) & 15)) == 0;
 }
@@ -774,6 +787,38 @@ __device__ __forceinline__ uint32_t hash_base(int64_t flat, uint32_t key) {
   return (uint32_t)flat * 0x9E3779B1u + (uint32_t)(flat >> 32) * 0x85EBCA77u + key;
 }
 
+// A block on its way through shared memory.
+template <bool BF16>
+struct alignas(16) Stage {
+  uint4 w[64], g[BF16 ? 32 : 64], m[16], r[16];
+};
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+template <bool BF16>
+__device__ __forceinline__ void fetch(Stage<BF16>& s, const Block& b) {
+  const int lane = threadIdx.x & 31;
+  copy16(&s.w[lane], b.w + 4 * lane);
+  copy16(&s.w[lane + 32], b.w + 4 * lane + 128);
+  copy16(&s.g[lane], b.g + 16 * lane);
+  if (!BF16) copy16(&s.g[BF16 ? 0 : lane + 32], b.g + 16 * lane + 512);
+  copy16(lane < 16 ? &s.m[lane] : &s.r[lane - 16], lane < 16 ? b.mq + 16 * lane : b.rq + 16 * (lane - 16));
+}
+__device__ __forceinline__ void copy4(void* to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+// The same from pointers that are aligned to four bytes only; the codes always are to more.
+template <bool BF16>
+__device__ __forceinline__ void fetch_narrow(Stage<BF16>& s, const Block& b) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) copy4(reinterpret_cast<float*>(s.w) + 32 * q + lane, b.w + 32 * q + lane);
+#pragma unroll
+  for (int q = 0; q < (BF16 ? 4 : 8); ++q)
+    copy4(reinterpret_cast<uint32_t*>(s.g) + 32 * q + lane, b.g + 4 * (32 * q + lane));
+  copy16(lane < 16 ? &s.m[lane] : &s.r[lane - 16], lane < 16 ? b.mq + 16 * lane : b.rq + 16 * (lane - 16));
+}
+__device__ __forceinline__ void end_fetch() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // A lane's eight elements as they lie in memory.
 template <bool BF16>
 struct Loaded {
@@ -781,9 +826,32 @@ struct Loaded {
   uint4 g16;
   uint2 m, r;
 };
+__device__ __forceinline__ F2 pair_of(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
+template <bool BF16>
+__device__ __forceinline__ void read_stage(const Stage<BF16>& s, Loaded<BF16>& x) {
+  const int lane = threadIdx.x & 31;
+  const uint4 a = s.w[2 * lane], c = s.w[2 * lane + 1];
+  x.w[0] = pair_of(a.x, a.y);
+  x.w[1] = pair_of(a.z, a.w);
+  x.w[2] = pair_of(c.x, c.y);
+  x.w[3] = pair_of(c.z, c.w);
+  if constexpr (BF16) {
+    x.g16 = s.g[lane];
+  } else {
+    const uint4 d = s.g[2 * lane], e = s.g[2 * lane + 1];
+    x.g[0] = pair_of(d.x, d.y);
+    x.g[1] = pair_of(d.z, d.w);
+    x.g[2] = pair_of(e.x, e.y);
+    x.g[3] = pair_of(e.z, e.w);
+  }
+  x.m = reinterpret_cast<const uint2*>(s.m)[lane];
+  x.r = reinterpret_cast<const uint2*>(s.r)[lane];
+}
+
+// s: where the block came from, and its weights go through again if it is not wide; null: it is wide.
 template <bool BF16>
 __device__ __forceinline__ void step_loaded(Loaded<BF16>& x, const Block& b, int& em, int& er, const Factors& f,
-                                            const Hyper& h) {
+                                            const Hyper& h, Stage<BF16>* s = nullptr) {
   const int lane = threadIdx.x & 31;
   F2 g[4], m[4], r[4];
   codes_to(x.m, m);
@@ -796,10 +864,23 @@ __device__ __forceinline__ void step_loaded(Loaded<BF16>& x, const Block& b, int
   }
   step_moments(x.w, g, m, r, em, er, f, h, hash_base(b.flat, f.s.key) + lane * 8 * 0x9E3779B1u, [](int q) { return q; },
                [&] {
-                 st32(b.w + 8 * lane, x.w);
-                 if (b.b)
-                   *reinterpret_cast<uint4*>(b.b + 8 * lane) =
-                       make_uint4(bf16_pair(x.w[0]), bf16_pair(x.w[1]), bf16_pair(x.w[2]), bf16_pair(x.w[3]));
+                 if (!s) {
+                   st32(b.w + 8 * lane, x.w);
+                   if (b.b)
+                     *reinterpret_cast<uint4*>(b.b + 8 * lane) =
+                         make_uint4(bf16_pair(x.w[0]), bf16_pair(x.w[1]), bf16_pair(x.w[2]), bf16_pair(x.w[3]));
+                   return;
+                 }
+                 ulonglong2* to = reinterpret_cast<ulonglong2*>(s->w) + 2 * lane;
+                 to[0] = make_ulonglong2(x.w[0].v, x.w[1].v);
+                 to[1] = make_ulonglong2(x.w[2].v, x.w[3].v);
+                 __syncwarp();
+#pragma unroll
+                 for (int q = 0; q < 8; ++q) {
+                   const float w = reinterpret_cast<const float*>(s->w)[32 * q + lane];
+                   b.w[32 * q + lane] = w;
+                   if (b.b) b.b[32 * q + lane] = bf16_bits(w);
+                 }
                });
   *reinterpret_cast<uint2*>(b.mq + 8 * lane) = to_codes(m);
   *reinterpret_cast<uint2*>(b.rq + 8 * lane) = to_codes(r);
@@ -855,46 +936,6 @@ __device__ __forceinline__ void step_block(const Block& b, int& em, int& er, con
   }
 }
 
-// A block on its way through shared memory.
-template <bool BF16>
-struct alignas(16) Stage {
-  uint4 w[64], g[BF16 ? 32 : 64], m[16], r[16];
-};
-__device__ __forceinline__ void copy16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
-}
-template <bool BF16>
-__device__ __forceinline__ void fetch(Stage<BF16>& s, const Block& b) {
-  const int lane = threadIdx.x & 31;
-  copy16(&s.w[lane], b.w + 4 * lane);
-  copy16(&s.w[lane + 32], b.w + 4 * lane + 128);
-  copy16(&s.g[lane], b.g + 16 * lane);
-  if (!BF16) copy16(&s.g[BF16 ? 0 : lane + 32], b.g + 16 * lane + 512);
-  copy16(lane < 16 ? &s.m[lane] : &s.r[lane - 16], lane < 16 ? b.mq + 16 * lane : b.rq + 16 * (lane - 16));
-}
-__device__ __forceinline__ void end_fetch() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ F2 pair_of(uint32_t a, uint32_t b) { return f2(__uint_as_float(a), __uint_as_float(b)); }
-template <bool BF16>
-__device__ __forceinline__ void read_stage(const Stage<BF16>& s, Loaded<BF16>& x) {
-  const int lane = threadIdx.x & 31;
-  const uint4 a = s.w[2 * lane], c = s.w[2 * lane + 1];
-  x.w[0] = pair_of(a.x, a.y);
-  x.w[1] = pair_of(a.z, a.w);
-  x.w[2] = pair_of(c.x, c.y);
-  x.w[3] = pair_of(c.z, c.w);
-  if constexpr (BF16) {
-    x.g16 = s.g[lane];
-  } else {
-    const uint4 d = s.g[2 * lane], e = s.g[2 * lane + 1];
-    x.g[0] = pair_of(d.x, d.y);
-    x.g[1] = pair_of(d.z, d.w);
-    x.g[2] = pair_of(e.x, e.y);
-    x.g[3] = pair_of(e.z, e.w);
-  }
-  x.m = reinterpret_cast<const uint2*>(s.m)[lane];
-  x.r = reinterpret_cast<const uint2*>(s.r)[lane];
-}
-
 // The blocks of the flat state go to the warps in fours, the scales of which are one word.  (Single
 // bytes, written among other warps' reads of their sector, took half of the step.)  A warp
 // has its next block on the way to shared memory while it steps one, and waits for no
@@ -904,7 +945,10 @@ __device__ __forceinline__ void read_stage(const Stage<BF16>& s, Loaded<BF16>& x
 //
 // The pointers in wp, gp, cp are those of the tensors less their offset in the flat state, so that
 // a tensor's number is all that a block has to look up.
-template <bool BF16, int K>
+//
+// NARROW: some tensor's pointers are not wide; a kernel of its own, since with that path the wide
+// ones take 3 % longer.  20M parameters without gaps: 85 us (97 us by single elements).
+template <bool BF16, bool NARROW, int K>
 __global__ void __launch_bounds__(kThreads, 4) adamw_8bit_kernel(ListTables t, const __grid_constant__ Pointers<K> wp,
                                                                  const __grid_constant__ Pointers<K> gp,
                                                                  const __grid_constant__ Pointers<K> cp, int copies,
@@ -928,23 +972,20 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_8bit_kernel(ListTables t, c
   Block b;
   b.flat = (4 * (int64_t)four + j0) * kQBlock;
   const int p = same(t.fours[four]);
-  bool through = false;   // shared memory
+  bool through = false, broad = false;   // through shared memory; by 16 bytes
   if (p >= 0) {
     at(b, p);
-    through = wide<BF16>(b.w, b.g, b.b);
-    if (through) fetch(stages[warp][j0 & 1], b);
+    broad = wide<BF16>(b.w, b.g, b.b);
+    through = broad || (NARROW && (!BF16 || (reinterpret_cast<uintptr_t>(b.g) & 3) == 0));
+    if (broad) fetch(stages[warp][j0 & 1], b);
+    else if (NARROW && through) fetch_narrow(stages[warp][j0 & 1], b);
   }
   end_fetch();
   wait_for_previous();
-  Factors f;
-  f.coef = t.result->coef;
-  f.huge = !(t.result->norm * f.coef < kGradMax);   // no element exceeds the norm
-  if (p >= 0) {
-    f.s = step[p];
-    if (t.skip[p]) {
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      return;
-    }
+  Factors f = factors_of(t, step, p);
+  if (p >= 0 && __ldcg(&t.skip[p])) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
   }
   uint32_t ms = reinterpret_cast<const uint32_t*>(st.ms)[four], rs = reinterpret_cast<const uint32_t*>(st.rs)[four];
   int em, er;
@@ -963,7 +1004,10 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_8bit_kernel(ListTables t, c
       next.mq += kQBlock;
       next.rq += kQBlock;
       next.flat += kQBlock;
-      if (j + 1 < j1) fetch(stages[warp][(j + 1) & 1], next);
+      if (j + 1 < j1) {
+        if (!NARROW || broad) fetch(stages[warp][(j + 1) & 1], next);
+        else fetch_narrow(stages[warp][(j + 1) & 1], next);
+      }
       end_fetch();
       asm volatile("cp.async.wait_group 1;" ::: "memory");   // all but the latest
       __syncwarp();
@@ -971,7 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_8bit_kernel(ListTables t, c
       read_stage<BF16>(stages[warp][j & 1], x);
       em = ms >> (8 * j) & 255;
       er = rs >> (8 * j) & 255;
-      step_loaded<BF16>(x, b, em, er, f, h);
+      step_loaded<BF16>(x, b, em, er, f, h, !NARROW || broad ? nullptr : &stages[warp][j & 1]);
       put_scales(j);
       __syncwarp();   // all lanes have read their stage before it is filled again
       b = next;
@@ -986,8 +1030,8 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_8bit_kernel(ListTables t, c
       if (p < 0) {   // fours of several tensors, or at the end of one
         if (blk >= t.nqblocks) break;
         own = t.owner[blk];
-        if (own < p0 || own >= p0 + np || t.skip[own]) continue;
-        f.s = step[own];
+        if (own < p0 || own >= p0 + np || __ldcg(&t.skip[own])) continue;
+        f.s = step_of(step, own);
         b.len = (int)min((int64_t)kQBlock, t.ends[own] - b.flat);
       }
       at(b, own);
@@ -1131,9 +1175,8 @@ __global__ void __launch_bounds__(32 * kSmallWarps)
         for (int i = lane; i < c.len; i += 32) store1<BF16>(g, i, load1<BF16>(g, i) * coef);
         continue;
       }
-      const float4 s = __ldcg(reinterpret_cast<const float4*>(adv.out + c.param));
       Factors f;
-      f.s = ListStep{s.x, s.y, s.z, __float_as_uint(s.w)};
+      f.s = step_of(adv.out, c.param);
       f.coef = coef;
       f.huge = !(norm * coef < (double)kGradMax);
       Block k;
@@ -1324,7 +1367,12 @@ cudaError_t launch_adamw_8bit(const ListTables& t, float* const* w, const void* 
     const Pointers<K> aw = less(w, 4), ag = less(g, bf16 ? 2 : 4), ac = copies ? less(copies, 2) : Pointers<K>{};
     const int per = nq < kSms * 3 * kListWarps ? 1 : 4;
     const int ctas = (nq * (4 / per) + kListWarps - 1) / kListWarps;
-    return launch_early(bf16 ? adamw_8bit_kernel<true, K> : adamw_8bit_kernel<false, K>, ctas, s, t, aw, ag, ac,
+    bool narrow = false;
+    for (int i = p0; i < p0 + np; ++i)
+      narrow |= !(bf16 ? wide<true> : wide<false>)(w[i], g[i], copies ? copies[i] : nullptr);
+    auto* kernel = narrow ? (bf16 ? adamw_8bit_kernel<true, true, K> : adamw_8bit_kernel<false, true, K>)
+                          : (bf16 ? adamw_8bit_kernel<true, false, K> : adamw_8bit_kernel<false, false, K>);
+    return launch_early(kernel, ctas, s, t, aw, ag, ac,
                         (int)(copies != nullptr), p0, np, q0, nq, per, st, step, h);
   });
 }

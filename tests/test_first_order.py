@@ -344,7 +344,7 @@ SETS = {
     "layer": [512 * 512, 512 * 1024, 512],
     "large edges": [8191, 8192, 8193, 1, 16384 + 255, 131072, 255, 50003],
 }
-# lists of up to 131072 elements take one launch, larger ones two: `more` brings a list over
+# lists of up to 65536 elements take one launch, larger ones two: `more` brings a list over
 
 
 @gpu
