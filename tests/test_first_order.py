@@ -465,7 +465,7 @@ def codes_of_f32(x, bits, square):
 
 @gpu
 @pytest.mark.parametrize("gdt", ["f32", "bf16"])
-@pytest.mark.parametrize("n,shift", [(1 << 22, 0), (1 << 20, 1), (40000, 0), (40000, 3)])
+@pytest.mark.parametrize("n,shift", [(1 << 22, 0), (1 << 20, 1), (1 << 20, 2), (5000001, 2), (40000, 0), (40000, 3)])
 def test_8bit_codes_are_those_of_operations_rounded_one_by_one(cuda, gdt, n, shift):
     """Every code equal, with no tolerance: a product fused with its sum changes a last bit in a fifth of the moments, and
     the code of about one element in a million; two steps on, at both alignments and in both kernels."""
