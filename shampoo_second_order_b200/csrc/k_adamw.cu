@@ -202,16 +202,17 @@ __global__ void __launch_bounds__(kThreads, 4) list_norm_kernel(ListTables t, co
                                                                 int p0, int np, int c0, int nc, int b0, double max_norm,
                                                                 ListAdvance adv) {
   using V = Vectors<BF16>;
-  __shared__ double red[kListWarps];
+  __shared__ double red[2][kListWarps];
   __shared__ bool last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int i0 = c0 + (int)((int64_t)nc * blockIdx.x / gridDim.x);
+  const int i1 = c0 + (int)((int64_t)nc * (blockIdx.x + 1) / gridDim.x);
+  ListChunk next = t.gchunks[i0];
   wait_for_previous();
   let_next_start();
   const unsigned pass = t.result->pass;
-  const int i0 = c0 + (int)((int64_t)nc * blockIdx.x / gridDim.x);
-  const int i1 = c0 + (int)((int64_t)nc * (blockIdx.x + 1) / gridDim.x);
   double total = 0.0, sum = 0.0;
-  bool bad = false;
-  ListChunk next = t.gchunks[i0];
+  int turn = 0;
   for (int i = i0; i < i1; ++i) {
     const ListChunk c = next;
     const V vec(ptr.p[c.param - p0], c.start, c.len);
@@ -222,9 +223,10 @@ __global__ void __launch_bounds__(kThreads, 4) list_norm_kernel(ListTables t, co
       u[k] = v < vec.nvec ? *vec.at(v) : make_uint4(0, 0, 0, 0);
     }
     if (i + 1 < i1) next = t.gchunks[i + 1];
+    bool bad = false;
     if (const void* one = vec.single()) {
       const float x = load1<BF16>(one, 0);
-      bad |= !isfinite(x);
+      bad = !isfinite(x);
       sum += (double)x * x;
     }
     constexpr int G = 16 / V::E;   // vectors of sixteen elements
@@ -246,24 +248,25 @@ __global__ void __launch_bounds__(kThreads, 4) list_norm_kernel(ListTables t, co
         }
       }
     }
-    const bool ends = i + 1 == i1 || next.param != c.param;
-    if (ends) {
-      sum = block_sum(sum, red);
-      const bool any = __syncthreads_or(bad);
+    if (bad) sum = nan("");   // finite squares do not add up to one in 64 bits
+    const bool end = i + 1 == i1;
+    if (end && adv.step)
+      for (int p = blockIdx.x * kThreads + threadIdx.x; p < np; p += gridDim.x * kThreads) step_factors(adv, p0 + p);
+    double run = 0.0;   // up to here, in thread 0
+    if (end || next.param != c.param) {
+      sum = warp_sum(sum);
+      if (lane == 0) red[turn][warp] = sum;
+      __syncthreads();
+      if (warp == 0) run = warp_sum(lane < kListWarps ? red[turn][lane] : 0.0);
       if (threadIdx.x == 0) {
-        total += sum;
-        if (any) t.mark[c.param] = t.result->bad = pass;
+        total += run;
+        if (isnan(run)) t.mark[c.param] = t.result->bad = pass;
       }
-    }
-    if (threadIdx.x == 0) t.partial[i] = ends ? sum : 0.0;
-    if (ends) {
+      turn ^= 1;   // the other warps may write the next run's sums while warp 0 reads these
       sum = 0.0;
-      bad = false;
     }
+    if (threadIdx.x == 0) t.partial[i] = run;
   }
-  if (adv.step)
-    for (int p = blockIdx.x * kThreads + threadIdx.x; p < np; p += gridDim.x * kThreads) step_factors(adv, p0 + p);
-  __syncthreads();
   if (threadIdx.x == 0) {
     t.csum[b0 + blockIdx.x] = total;
     // releases what this CTA has written, and acquires what those before it have
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 4) list_norm_kernel(ListTables t, co
   }
   __syncthreads();
   if (!last) return;
-  close_pass(t, pass, max_norm, adv, red);
+  close_pass(t, pass, max_norm, adv, red[0]);
 }
 
 // The chunks in the reverse of the norm's order: what it read last is still in L2.
