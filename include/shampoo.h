@@ -580,7 +580,7 @@ shampoo_status shampoo_adamw_step(shampoo_adamw* adamw, float* const* params,
  * until shampoo_adamw_destroy.  The moments of all tensors lie in one array each;
  * tensor i's begin at element shampoo_adamw_offset(i), a multiple of 256, and
  * what lies between one tensor's end and the next one's beginning is zero and must
- * stay so.
+ * stay so.  Step counts are >= 0, codes of sqrt(v) not negative, and no code a NaN.
  */
 enum {
   SHAMPOO_ADAMW_NORM = 0,      /* float [1]: the gradient norm of the last step  */

@@ -57,13 +57,14 @@ def _build_tensors(verbose: bool) -> None:
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-           "-isystem", sysconfig.get_path("include"), os.path.join(CSRC, "tensors.cpp"), "-o", TENSORS,
+           "-isystem", sysconfig.get_path("include"), os.path.join(CSRC, "tensors.cpp"), "-o", TENSORS + ".new",
            "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on tensors.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(TENSORS + ".new", TENSORS)   # a process may have the old one loaded
 
 
 def build(verbose: bool = False, ptxas_v: bool = False) -> str:

@@ -111,8 +111,7 @@ shampoo_status allocate(List* l, const Layout& y) {
 void release(List* l) {
   if (!l->memory) return;
   OnDevice on(l->device);
-  cudaStreamSynchronize(l->stream);
-  cudaFree(l->memory);
+  cudaFree(l->memory);   // waits for the device; the stream may be gone by now
 }
 
 // Checks the list's sizes, then its tables on the host and the device.  The
@@ -266,7 +265,11 @@ shampoo_status guarded(List* l, F&& f) {
   try {
     return f();
   } catch (const std::bad_alloc&) {
-    return l ? SHAMPOO_ENOMEM : refuse(nullptr, SHAMPOO_ENOMEM, "out of host memory");
+    try {
+      return refuse(l, SHAMPOO_ENOMEM, "out of host memory");
+    } catch (...) {
+      return SHAMPOO_ENOMEM;
+    }
   } catch (...) {
     return SHAMPOO_ECUDA;
   }

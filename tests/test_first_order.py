@@ -617,6 +617,56 @@ def test_adamw_in_a_graph_and_on_other_streams(cuda, state, own_stream, more):
 
 
 @gpu
+def test_many_contexts_at_once(cuda):
+    """Sixteen contexts of one to 1500 tensors, eager and as graphs, on five streams at a time: each ends where it ends
+    when it runs alone."""
+    import random
+    from shampoo_second_order_b200 import AdamW
+
+    def make(seed):
+        r = random.Random(seed)
+        n, total = r.choice([1, 3, 40, 300, 1500]), r.choice([500, 60000, 70000, 900000, 3000000])
+        sizes = [max(1, int(total / n * r.uniform(0.2, 2.0))) for _ in range(n)]
+        gdt, state = r.choice(["f32", "bf16"]), r.choice(["f32", "8bit"])
+        gen = torch.Generator("cuda").manual_seed(seed)
+        w = torch.randn(sum(sizes), device="cuda", generator=gen) * 0.02
+        g = (torch.randn(sum(sizes), device="cuda", generator=gen) * 1e-3).to(torch.bfloat16 if gdt == "bf16" else torch.float32)
+        b = torch.zeros(sum(sizes), device="cuda", dtype=torch.bfloat16)
+        opt = AdamW([(k,) for k in sizes], state=state, grad_dtype=gdt, max_norm=r.choice([0, 0.1]), seed=seed)
+        lists = [list(torch.split(x, sizes)) for x in (w, g, b)]
+        return opt, lambda: opt.step(lists[0], lists[1], 1e-3, copies=lists[2]), w, b
+
+    def ends(opt, step, w, b):
+        return [x.view(torch.uint8).clone() for x in (w, b, *opt.state_tensors().values())]
+
+    want = []
+    for seed in range(16):
+        alone = make(seed)
+        for _ in range(5):
+            alone[1]()
+        want.append(ends(*alone))
+    runs, calls = [make(seed) for seed in range(16)], []
+    torch.cuda.synchronize()
+    for seed, run in enumerate(runs):
+        if seed % 3:
+            calls.append(run[1])
+            continue
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run[1]()
+        calls.append(graph.replay)
+    streams, rnd = [torch.cuda.Stream() for _ in range(5)], random.Random(0)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for seed in rnd.sample(range(16), 16):
+            with torch.cuda.stream(streams[seed % 5]):
+                calls[seed]()
+    torch.cuda.synchronize()
+    for seed, run in enumerate(runs):
+        assert all(torch.equal(x, y) for x, y in zip(want[seed], ends(*run))), seed
+
+
+@gpu
 def test_adamw_refuses_lists_that_overlap(cuda):
     from shampoo_second_order_b200 import AdamW, GradClip
     buf, g = torch.zeros(100, device="cuda"), torch.zeros(2, 40, device="cuda")
